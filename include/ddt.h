@@ -13,6 +13,14 @@
  *   ddt_kv_write_block  the tree block's KV rows into the cache after the prefix
  *   ddt_decode_step  all of the above chained on the device for one decode step
  *
+ * and, over a latent cache held in 8 bits in pages of 64 rows (see "The paged
+ * 8-bit latent cache"):
+ *
+ *   ddt_kv_pages       block tables and slot maps from the requests' lengths
+ *   ddt_kv_write_q8    bf16 rows quantised into their pages
+ *   ddt_verify_attn_q8 the tree-verify attention over those pages
+ *   ddt_kv_compact_q8  gather of the accepted rows, in place
+ *
  * Sources (cited by page title and section):
  *   [Race Conditions]  "Race Conditions, Buffer Aliasing, and the Architecture of
  *                      a Native DDTree Inference Engine"
@@ -81,6 +89,8 @@ typedef enum ddt_status {
 #define DDT_REQ_BAD_PREFIX 4   /* prefix_len < 0 or prefix_len + rows > capacity   */
 #define DDT_REQ_BAD_LENGTH 5   /* accept_len not in [1, q_len]                     */
 #define DDT_REQ_BAD_LP 6       /* a log-probability given to the tree build is not finite */
+#define DDT_REQ_NO_PAGES 7     /* the free pages do not reach this request         */
+#define DDT_REQ_NOT_FINITE 8   /* a row given to ddt_kv_write_q8 held NaN or an infinity */
 
 typedef enum ddt_dtype { DDT_F32 = 0, DDT_BF16 = 1 } ddt_dtype;
 
@@ -455,6 +465,185 @@ typedef struct ddt_decode_args {
 } ddt_decode_args;
 
 DDT_API ddt_status ddt_decode_step(const ddt_decode_args* args, ddt_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* The paged 8-bit latent cache                                             */
+/* ------------------------------------------------------------------------ */
+/* The latent cache of ddt_verify_attn at half the bytes, its rows scattered over
+ * a pool of pages that requests share.  The pages of the sources describe only
+ * the contiguous bf16 cache; this form exists for users of the library whose
+ * requests grow and shrink in one pool of memory.
+ *
+ * A page holds DDT_PAGE_ROWS = 64 rows of 512 latent and 64 rope values in e4m3
+ * (4-bit exponent, 3-bit mantissa, largest value 448, no infinities) and has one
+ * fp32 scale: row r of page p stands for the values
+ *     scales[p] * c_kv[p, r, :]   and   scales[p] * k_rope[p, r, :].
+ * Scales are powers of two, at least 2^-40, so that a change of scale only shifts
+ * exponents: it alters a value only where it falls below e4m3's normal range
+ * (2^-6), by at most half a step there (2^-10 times the new scale).  Since e4m3
+ * is a floating format, one scale over latent and rope costs nothing while their
+ * magnitudes lie within 2^14 of each other.
+ *
+ * Cache row j of request b is row j % 64 of page block_table[b * max_blocks + j / 64].
+ * The pages in use must be distinct, within a request and between requests (calls
+ * that only read may share them); a page index outside [0, num_pages) is never
+ * followed, and gives DDT_REQ_BAD_INDEX where a call needs that page.
+ *
+ * Strides are in elements (= bytes), multiples of 16; bases are 16-byte aligned;
+ * a row is 512 / 64 contiguous values.  One allocation of 576-byte rows serves
+ * both arrays (k_rope = c_kv + 512). */
+#define DDT_PAGE_ROWS 64
+
+typedef struct ddt_q8_cache {
+  void* c_kv;                               /* e4m3 [num_pages, 64, 512], strided */
+  void* k_rope;                             /* e4m3 [num_pages, 64, 64], strided  */
+  float* scales;                            /* fp32 [num_pages]                   */
+  const int32_t* block_table;               /* int32 [B, max_blocks]              */
+  int64_t ckv_page_stride, ckv_row_stride;
+  int64_t kr_page_stride, kr_row_stride;
+  int32_t num_pages;
+  int32_t max_blocks;                       /* at most 2^24 */
+} ddt_q8_cache;
+
+/* ------------------------------------------------------------------------ */
+/* ddt_kv_pages                                                             */
+/* ------------------------------------------------------------------------ */
+/* Block tables and slot maps from the requests' lengths, on the device.
+ *
+ * Request b holds prefix_lens[b] rows and is to hold n_b more: n_b =
+ * row_start[b+1] - row_start[b], or q_len for every request with row_start NULL.
+ * It needs need_b = ceil((prefix_lens[b] + n_b) / 64) pages and holds
+ * n_blocks[b], listed in block_table[b, 0 .. n_blocks[b]).  The free pages are the
+ * stack free_pages[0 .. *n_free).
+ *   1. Every request that holds more than it needs gives the rest back; its table
+ *      entries past need_b become -1.
+ *   2. Requests that need more take pages from the top of the stack, in the order
+ *      of their index: request b is served iff the pages wanted by requests
+ *      0 .. b together do not exceed the free ones (counting those just given
+ *      back).  A request that is not served keeps its table (DDT_REQ_NO_PAGES).
+ *   3. slots[row_start[b] + i] = page * 64 + offset of row prefix_lens[b] + i, for
+ *      writers of the caller's own; -1 for a request with a non-zero status.
+ * Pages given back are stacked so that taking as many again, by the same
+ * requests, returns the same pages: a step taken back restores the state.  The
+ * result does not depend on timing.
+ *
+ * block_table int32 [B, max_blocks], n_blocks int32 [B], free_pages int32
+ * [num_pages] and n_free int32 [1] are updated in place; slots int64 [n_rows] or
+ * NULL (n_rows = the rows of all requests; rows past it are not written);
+ * row_start int32 [B + 1] or NULL; status int32 [B] or NULL: DDT_REQ_NO_PAGES,
+ * DDT_REQ_BAD_LENGTH (n_b < 0), DDT_REQ_BAD_PREFIX (prefix_lens[b] < 0, or more
+ * than max_blocks * 64 rows in all) or DDT_REQ_BAD_INDEX (n_blocks[b] outside
+ * [0, max_blocks]; or, for every request, n_free outside [0, num_pages] or more
+ * pages given back than the stack has room for, in which case nothing is
+ * changed).  A request with a non-zero status keeps its pages.
+ * Errors: B, q_len, n_rows, num_pages or max_blocks < 0, max_blocks > 2^24, or a
+ * required pointer NULL with B > 0 -> DDT_ERR_INVALID_ARG.  B = 0 is a no-op. */
+DDT_API ddt_status ddt_kv_pages(const int32_t* prefix_lens, const int32_t* row_start, int32_t B,
+                          int32_t q_len, int64_t n_rows, int32_t num_pages, int32_t max_blocks,
+                          int32_t* block_table, int32_t* n_blocks, int32_t* free_pages,
+                          int32_t* n_free, int64_t* slots, int32_t* status,
+                          ddt_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* ddt_kv_write_q8                                                          */
+/* ------------------------------------------------------------------------ */
+/* Quantises bf16 rows into the cache behind each request's prefix: the tree block
+ * of a step, a prompt, or one token.  Row i of request b (i < n_b, counted as in
+ * ddt_kv_pages) goes to cache row prefix_lens[b] + i.
+ *
+ * For each page that a request's rows reach, fit = the smallest power of two, at
+ * least 2^-40, with amax <= 448 * fit over the page's new rows (both parts):
+ *   - the rows start at the page's row 0:  scale = fit;
+ *   - they start behind live rows:         scale = max(old scale, fit); when that
+ *     is larger than the old scale, the live rows before them are rescaled.
+ * New rows are stored as x / scale, rounded to nearest even.  Rows of a page
+ * behind the last one written keep their bytes.
+ * A NaN is stored as 0 and an infinity as the largest value of its sign (amax is
+ * taken over finite values), so what this call writes is always finite; the
+ * request's status is then DDT_REQ_NOT_FINITE, and its other rows are written.
+ *
+ * rows_ckv bf16 [n_rows, 512] and rows_krope bf16 [n_rows, 64], contiguous,
+ * 16-byte aligned, request b's from row_start[b] (or b * q_len) on.  max_rows: a
+ * bound on every n_b known to the host (it sizes the launch; q_len with row_start
+ * NULL).  status int32 [B] or NULL: DDT_REQ_NOT_FINITE, or DDT_REQ_BAD_LENGTH
+ * (n_b < 0, n_b > max_rows or rows outside [0, n_rows)), DDT_REQ_BAD_PREFIX,
+ * DDT_REQ_BAD_INDEX (a page index of its rows), which write nothing for that
+ * request.  B = 0 or max_rows = 0 is a no-op (a given status is set). */
+DDT_API ddt_status ddt_kv_write_q8(const ddt_q8_cache* cache, const int32_t* prefix_lens,
+                          const int32_t* row_start, int32_t B, int32_t q_len, int32_t max_rows,
+                          int64_t n_rows, const void* rows_ckv, const void* rows_krope,
+                          int32_t* status, ddt_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* ddt_verify_attn_q8                                                       */
+/* ------------------------------------------------------------------------ */
+/* ddt_verify_attn over the paged 8-bit cache: the same formula on the values that
+ * the cache stands for, with the tree block at cache rows P .. P+q_len-1 (q_len 1
+ * with mask word 1 is a plain decode step).  Queries are bf16 and enter as the sum
+ * of two e4m3 terms under a power-of-two scale per row (exact to 2^-19 of the
+ * row's largest value); softmax weights likewise (relative error at most 2^-8,
+ * as a bf16 weight's); scores, sums and the output accumulate in fp32.
+ *
+ * out is bf16 [B, q_len, 64, 512] (the weights' 8 bits would not fill an fp32
+ * output), lse fp32 [B, q_len, 64] or NULL, with the meaning of ddt_verify_attn;
+ * a row that sees no key gives 0 and -inf.  Cache rows at or past P + q_len are
+ * never read.  A NaN byte in a row of the request makes the whole request's
+ * outputs NaN at that column, whether a node sees the row or not (0 * NaN);
+ * ddt_kv_write_q8 never stores one.
+ * Splits, workspace and max_prefix as for ddt_verify_attn.
+ * status int32 [B] or NULL: DDT_REQ_BAD_PREFIX (P < 0 or P + q_len > max_blocks *
+ * 64), outputs of that request unwritten; DDT_REQ_BAD_INDEX (a page index of rows
+ * < P + q_len): those rows count as zeros.
+ * Errors as for ddt_verify_attn. */
+typedef struct ddt_attn_q8_args {
+  int32_t B;          /* requests, >= 0                                        */
+  int32_t q_len;      /* tree nodes per request, 1..128                         */
+  int32_t num_heads;  /* must be 64                                             */
+  int32_t d_latent;   /* must be 512                                            */
+  int32_t d_rope;     /* must be 64                                             */
+  int32_t max_prefix; /* host-known upper bound on prefix_lens (plans splits)   */
+  ddt_q8_cache cache;
+  const int32_t* prefix_lens; /* int32 [B]                                      */
+  const void* q_lat;  /* bf16 [B, q_len, 64, 512], contiguous                   */
+  const void* q_rope; /* bf16 [B, q_len, 64, 64], contiguous                    */
+  const uint64_t* mask; /* uint64 [B, q_len, W] from ddt_build_mask             */
+  void* out;          /* bf16 [B, q_len, 64, 512]                               */
+  float* lse;         /* fp32 [B, q_len, 64] or NULL                            */
+  void* workspace;    /* scratch for split partials, or NULL                    */
+  size_t workspace_bytes;
+  int32_t* status;    /* int32 [B] or NULL                                      */
+  float softmax_scale; /* > 0 and finite                                        */
+  int32_t num_splits; /* 0 = choose automatically; otherwise 1..64              */
+} ddt_attn_q8_args;
+
+/* Bytes of workspace and number of KV splits the call will use (sizes only;
+ * invalid sizes give 0 and 1). */
+DDT_API size_t ddt_verify_attn_q8_workspace_size(const ddt_attn_q8_args* args);
+DDT_API int32_t ddt_verify_attn_q8_num_splits(const ddt_attn_q8_args* args);
+
+DDT_API ddt_status ddt_verify_attn_q8(const ddt_attn_q8_args* args, ddt_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* ddt_kv_compact_q8                                                        */
+/* ------------------------------------------------------------------------ */
+/* ddt_kv_compact on the paged 8-bit cache, in place and race-free for any path:
+ *   for i < accept_len[b]:  row P+i stands for what row P+path[b,i] stood for
+ *   new_prefix_lens[b] = P + accept_len[b]
+ * A page that rows move into takes the largest scale among its own and those
+ * rows' pages; when that raises it, its other rows are rescaled and so keep their
+ * values (as ddt_kv_write_q8 does).  Rows that keep their place and scale are not
+ * rewritten.  Pages that end up unused are given back by the next ddt_kv_pages.
+ *
+ * path int32 [B, q_len], accept_len, prefix_lens int32 [B]; new_prefix_lens int32
+ * [B] or NULL (it may be prefix_lens itself); status int32 [B] or NULL:
+ * DDT_REQ_BAD_LENGTH, DDT_REQ_BAD_PREFIX (P < 0 or P + q_len > max_blocks * 64),
+ * DDT_REQ_BAD_INDEX (a path entry outside [0, q_len), or a page index of rows
+ * P .. P+q_len-1); a request with a non-zero status is left unchanged and its new
+ * prefix equals its old one.  Errors as for ddt_kv_compact. */
+DDT_API ddt_status ddt_kv_compact_q8(const ddt_q8_cache* cache, const int32_t* prefix_lens,
+                          const int32_t* path, const int32_t* accept_len, int32_t B,
+                          int32_t q_len, int32_t* new_prefix_lens, int32_t* status,
+                          ddt_stream_t stream);
 
 /* Human-readable name of a status code (static storage). */
 DDT_API const char* ddt_status_str(ddt_status status);

@@ -20,6 +20,8 @@ constexpr int kMaxSlots = 16;
 constexpr int kMaxContexts = 64;
 static_assert(kMaxSlots <= 32, "one bit per slot");
 
+constexpr int kMaxBlocks = 1 << 24;  // rows per request stay within 2^30
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Shared cache row checks of ddt_verify_attn and ddt_kv_compact.
@@ -31,6 +33,20 @@ bool cache_strides_ok(int B, int capacity, int64_t ckv_bs, int64_t ckv_rs, int64
                 kr_bs < static_cast<int64_t>(capacity) * kr_rs))
     return false;
   return true;
+}
+
+// Checks of the paged cache shared by its calls.
+bool q8_cache_ok(const ddt_q8_cache& c) {
+  if (c.num_pages < 1 || c.max_blocks < 1 || c.max_blocks > kMaxBlocks) return false;
+  if (!c.c_kv || !c.k_rope || !c.scales || !c.block_table) return false;
+  if (!aligned16(c.c_kv) || !aligned16(c.k_rope)) return false;
+  if ((c.ckv_page_stride | c.ckv_row_stride | c.kr_page_stride | c.kr_row_stride) % 16) return false;
+  if (c.ckv_row_stride < DDT_D_LATENT || c.kr_row_stride < DDT_D_ROPE) return false;
+  // tensor maps take strides below 2^40 bytes
+  if (c.ckv_row_stride >= (int64_t{1} << 33) || c.kr_row_stride >= (int64_t{1} << 33)) return false;
+  if (c.ckv_page_stride >= (int64_t{1} << 40) || c.kr_page_stride >= (int64_t{1} << 40)) return false;
+  return c.num_pages == 1 || (c.ckv_page_stride >= DDT_PAGE_ROWS * c.ckv_row_stride &&
+                              c.kr_page_stride >= DDT_PAGE_ROWS * c.kr_row_stride);
 }
 
 }  // namespace
@@ -276,6 +292,13 @@ static ddt_status check_attn_shape(const ddt_attn_args* a) {
   return DDT_OK;
 }
 
+// A positive, finite scale (and log2(e) times it): the kernels apply it after
+// taking the maximum of the raw scores, which needs scale > 0.
+static bool softmax_scale_ok(float scale) {
+  const float scale_log2 = scale * 1.4426950408889634f;
+  return scale > 0.0f && scale_log2 <= 3.402823466e38f;
+}
+
 static ddt_status check_attn_args(const ddt_attn_args* a) {
   const ddt_status shape = check_attn_shape(a);
   if (shape != DDT_OK) return shape;
@@ -290,10 +313,7 @@ static ddt_status check_attn_args(const ddt_attn_args* a) {
   if (!cache_strides_ok(a->B, a->capacity, a->ckv_batch_stride, a->ckv_row_stride,
                         a->kr_batch_stride, a->kr_row_stride))
     return DDT_ERR_INVALID_ARG;
-  // A positive, finite scale (and log2(e) times it): the kernel applies it after
-  // taking the maximum of the raw scores, which needs scale > 0.
-  const float scale_log2 = a->softmax_scale * 1.4426950408889634f;
-  if (!(a->softmax_scale > 0.0f) || !(scale_log2 <= 3.402823466e38f)) return DDT_ERR_INVALID_ARG;
+  if (!softmax_scale_ok(a->softmax_scale)) return DDT_ERR_INVALID_ARG;
   return DDT_OK;
 }
 
@@ -367,6 +387,110 @@ ddt_status ddt_kv_write_block(void* c_kv, void* k_rope, int64_t ckv_batch_stride
                             nullptr, status, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
     return DDT_ERR_CUDA;
   return DDT_OK;
+}
+
+ddt_status ddt_kv_pages(const int32_t* prefix_lens, const int32_t* row_start, int32_t B,
+                        int32_t q_len, int64_t n_rows, int32_t num_pages, int32_t max_blocks,
+                        int32_t* block_table, int32_t* n_blocks, int32_t* free_pages,
+                        int32_t* n_free, int64_t* slots, int32_t* status, ddt_stream_t stream) {
+  if (B < 0 || q_len < 0 || n_rows < 0 || num_pages < 0 || max_blocks < 0 ||
+      max_blocks > kMaxBlocks)
+    return DDT_ERR_INVALID_ARG;
+  if (B == 0) return DDT_OK;
+  if (!prefix_lens || !block_table || !n_blocks || !free_pages || !n_free)
+    return DDT_ERR_INVALID_ARG;
+  if (launch_kv_pages(prefix_lens, row_start, B, q_len, n_rows, num_pages, max_blocks, block_table,
+                      n_blocks, free_pages, n_free, slots, status,
+                      reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return DDT_ERR_CUDA;
+  return DDT_OK;
+}
+
+ddt_status ddt_kv_write_q8(const ddt_q8_cache* cache, const int32_t* prefix_lens,
+                           const int32_t* row_start, int32_t B, int32_t q_len, int32_t max_rows,
+                           int64_t n_rows, const void* rows_ckv, const void* rows_krope,
+                           int32_t* status, ddt_stream_t stream) {
+  if (!cache || B < 0 || q_len < 0 || max_rows < 0 || n_rows < 0) return DDT_ERR_INVALID_ARG;
+  if (!row_start) max_rows = q_len;
+  if (B == 0) return DDT_OK;
+  if (!q8_cache_ok(*cache) || !prefix_lens) return DDT_ERR_INVALID_ARG;
+  if (max_rows > 0 && n_rows > 0 && (!rows_ckv || !rows_krope)) return DDT_ERR_INVALID_ARG;
+  if (!aligned16(rows_ckv) || !aligned16(rows_krope)) return DDT_ERR_INVALID_ARG;
+  if (launch_kv_write_q8(*cache, prefix_lens, row_start, B, q_len, max_rows, n_rows,
+                         static_cast<const uint16_t*>(rows_ckv),
+                         static_cast<const uint16_t*>(rows_krope), status,
+                         reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return DDT_ERR_CUDA;
+  return DDT_OK;
+}
+
+ddt_status ddt_kv_compact_q8(const ddt_q8_cache* cache, const int32_t* prefix_lens,
+                             const int32_t* path, const int32_t* accept_len, int32_t B,
+                             int32_t q_len, int32_t* new_prefix_lens, int32_t* status,
+                             ddt_stream_t stream) {
+  if (!cache || B < 0) return DDT_ERR_INVALID_ARG;
+  if (q_len < 1 || q_len > DDT_MAX_Q_LEN) return DDT_ERR_UNSUPPORTED;
+  if (B == 0) return DDT_OK;
+  if (!q8_cache_ok(*cache) || !prefix_lens || !path || !accept_len) return DDT_ERR_INVALID_ARG;
+  if (launch_kv_compact_q8(*cache, prefix_lens, path, accept_len, B, q_len, new_prefix_lens,
+                           status, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return DDT_ERR_CUDA;
+  return DDT_OK;
+}
+
+// The sizes of a paged call in the form that the split plan takes.
+static ddt_status q8_attn_shape(const ddt_attn_q8_args* a, ddt_attn_args* plain) {
+  if (!a) return DDT_ERR_INVALID_ARG;
+  if (a->cache.max_blocks < 0 || a->cache.max_blocks > kMaxBlocks) return DDT_ERR_INVALID_ARG;
+  *plain = {};
+  plain->B = a->B;
+  plain->q_len = a->q_len;
+  plain->num_heads = a->num_heads;
+  plain->d_latent = a->d_latent;
+  plain->d_rope = a->d_rope;
+  plain->capacity = a->cache.max_blocks * DDT_PAGE_ROWS;
+  plain->max_prefix = a->max_prefix;
+  plain->num_splits = a->num_splits;
+  return check_attn_shape(plain);
+}
+
+int32_t ddt_verify_attn_q8_num_splits(const ddt_attn_q8_args* a) {
+  ddt_attn_args plain;
+  if (q8_attn_shape(a, &plain) != DDT_OK || plain.B == 0) return 1;
+  return verify_num_splits(plain, device_sm_count());
+}
+
+size_t ddt_verify_attn_q8_workspace_size(const ddt_attn_q8_args* a) {
+  ddt_attn_args plain;
+  if (q8_attn_shape(a, &plain) != DDT_OK || plain.B == 0) return 0;
+  return verify_workspace_bytes(plain, verify_num_splits(plain, device_sm_count()));
+}
+
+ddt_status ddt_verify_attn_q8(const ddt_attn_q8_args* a, ddt_stream_t stream) {
+  ddt_attn_args plain;
+  const ddt_status st = q8_attn_shape(a, &plain);
+  if (st != DDT_OK || a->B == 0) return st;
+  if (!q8_cache_ok(a->cache) || !a->prefix_lens || !a->q_lat || !a->q_rope || !a->mask || !a->out)
+    return DDT_ERR_INVALID_ARG;
+  if (!aligned16(a->q_lat) || !aligned16(a->q_rope) || !aligned16(a->out))
+    return DDT_ERR_INVALID_ARG;
+  if (plain.capacity < a->q_len) return DDT_ERR_INVALID_ARG;
+  if (!softmax_scale_ok(a->softmax_scale)) return DDT_ERR_INVALID_ARG;
+  int splits = verify_num_splits(plain, device_sm_count());
+  const size_t need = verify_workspace_bytes(plain, splits);
+  float* part_o = nullptr;
+  float* part_lse = nullptr;
+  if (splits > 1) {
+    if (!a->workspace || a->workspace_bytes < need ||
+        (reinterpret_cast<uintptr_t>(a->workspace) & 255u)) {
+      splits = 1;
+    } else {
+      part_o = static_cast<float*>(a->workspace);
+      part_lse = part_o + static_cast<size_t>(splits) * a->B * a->q_len * 64 * 512;
+    }
+  }
+  return launch_verify_attn_q8(*a, splits, part_o, part_lse,
+                               reinterpret_cast<cudaStream_t>(stream));
 }
 
 ddt_status ddt_decode_step(const ddt_decode_args* d, ddt_stream_t stream) {

@@ -20,10 +20,11 @@ _LIB = None
 
 DDT_OK, DDT_ERR_INVALID_ARG, DDT_ERR_UNSUPPORTED, DDT_ERR_CUDA, DDT_ERR_INPUT = range(5)
 REQ_OK, REQ_BAD_PARENT, REQ_BAD_INDEX, REQ_WALK_LIMIT, REQ_BAD_PREFIX, REQ_BAD_LENGTH, \
-    REQ_BAD_LP = range(7)
+    REQ_BAD_LP, REQ_NO_PAGES, REQ_NOT_FINITE = range(9)
 FAULT_WAIT_TIMEOUT = 1
 DDT_F32, DDT_BF16 = 0, 1
 NUM_HEADS, D_LATENT, D_ROPE, MAX_Q_LEN = 64, 512, 64, 128
+PAGE_ROWS = 64
 
 EXPORTED_SYMBOLS = (
     "ddt_tree_build", "ddt_build_mask", "ddt_verify_attn", "ddt_verify_attn_workspace_size",
@@ -31,6 +32,8 @@ EXPORTED_SYMBOLS = (
     "ddt_kv_write_block", "ddt_decode_step", "ddt_verify_attn_split_tail",
     "ddt_selftest_bounded_wait",
     "ddt_verify_attn_split_tail_workspace_size",
+    "ddt_kv_pages", "ddt_kv_write_q8", "ddt_verify_attn_q8", "ddt_verify_attn_q8_workspace_size",
+    "ddt_verify_attn_q8_num_splits", "ddt_kv_compact_q8",
     "ddt_status_str",
     "ddt_fault_flags", "ddt_version",
 )
@@ -67,6 +70,30 @@ class DecodeArgs(ctypes.Structure):
         ("next_token", ctypes.c_void_p), ("next_sibling", ctypes.c_void_p),
         ("n_nodes", ctypes.c_void_p), ("target_tokens", ctypes.c_void_p),
         ("path", ctypes.c_void_p), ("accept_len", ctypes.c_void_p), ("status", ctypes.c_void_p),
+    ]
+
+
+class Q8Cache(ctypes.Structure):
+    """Mirror of ddt_q8_cache."""
+    _fields_ = [
+        ("c_kv", ctypes.c_void_p), ("k_rope", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+        ("block_table", ctypes.c_void_p),
+        ("ckv_page_stride", ctypes.c_int64), ("ckv_row_stride", ctypes.c_int64),
+        ("kr_page_stride", ctypes.c_int64), ("kr_row_stride", ctypes.c_int64),
+        ("num_pages", ctypes.c_int32), ("max_blocks", ctypes.c_int32),
+    ]
+
+
+class AttnQ8Args(ctypes.Structure):
+    """Mirror of ddt_attn_q8_args."""
+    _fields_ = [
+        ("B", ctypes.c_int32), ("q_len", ctypes.c_int32), ("num_heads", ctypes.c_int32),
+        ("d_latent", ctypes.c_int32), ("d_rope", ctypes.c_int32), ("max_prefix", ctypes.c_int32),
+        ("cache", Q8Cache), ("prefix_lens", ctypes.c_void_p), ("q_lat", ctypes.c_void_p),
+        ("q_rope", ctypes.c_void_p), ("mask", ctypes.c_void_p), ("out", ctypes.c_void_p),
+        ("lse", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t), ("status", ctypes.c_void_p),
+        ("softmax_scale", ctypes.c_float), ("num_splits", ctypes.c_int32),
     ]
 
 
@@ -112,6 +139,18 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.ddt_decode_step.restype = i32
     lib.ddt_selftest_bounded_wait.argtypes = [ctypes.c_uint32, V, V]
     lib.ddt_selftest_bounded_wait.restype = i32
+    lib.ddt_kv_pages.argtypes = [V, V, i32, i32, i64, i32, i32, V, V, V, V, V, V, V]
+    lib.ddt_kv_pages.restype = i32
+    lib.ddt_kv_write_q8.argtypes = [ctypes.POINTER(Q8Cache), V, V, i32, i32, i32, i64, V, V, V, V]
+    lib.ddt_kv_write_q8.restype = i32
+    lib.ddt_kv_compact_q8.argtypes = [ctypes.POINTER(Q8Cache), V, V, V, i32, i32, V, V, V]
+    lib.ddt_kv_compact_q8.restype = i32
+    lib.ddt_verify_attn_q8.argtypes = [ctypes.POINTER(AttnQ8Args), V]
+    lib.ddt_verify_attn_q8.restype = i32
+    lib.ddt_verify_attn_q8_workspace_size.argtypes = [ctypes.POINTER(AttnQ8Args)]
+    lib.ddt_verify_attn_q8_workspace_size.restype = ctypes.c_size_t
+    lib.ddt_verify_attn_q8_num_splits.argtypes = [ctypes.POINTER(AttnQ8Args)]
+    lib.ddt_verify_attn_q8_num_splits.restype = i32
     lib.ddt_status_str.argtypes = [i32]
     lib.ddt_status_str.restype = ctypes.c_char_p
     lib.ddt_fault_flags.argtypes = [ctypes.POINTER(ctypes.c_uint32), i32]
@@ -394,6 +433,228 @@ def decode_step_args(state: dict, step: dict, bufs: dict, softmax_scale: float,
 def decode_step(args: DecodeArgs, stream=None) -> None:
     """Launch one chained decode step (see decode_step_args)."""
     _check(load().ddt_decode_step(ctypes.byref(args), _stream(stream)), "ddt_decode_step")
+
+
+# ---------------------------------------------------------------------------
+# The paged 8-bit latent cache
+# ---------------------------------------------------------------------------
+
+class _OnDevice:
+    """Launches go to the device of the call's tensors, on its current stream (or the
+    given one), whatever device is current; torch's current device is left as it was."""
+
+    __slots__ = ("guard", "stream")
+
+    def __init__(self, device: torch.device, stream):
+        self.guard = (None if device.index == torch.cuda.current_device()
+                      else torch.cuda.device(device))
+        self.stream = (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self.stream
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _need(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape, device, contiguous=True):
+    """The data pointer of an argument of the paged calls (0 for None), once its type,
+    device, shape (None: any size) and layout are what the call takes."""
+    if t is None:
+        return 0
+    if t.device != device or t.dtype is not dtype:
+        raise DdtError(f"{name} must be {dtype} on {device}, got {t.dtype} on {t.device}")
+    if t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
+        want = "x".join("any" if w is None else str(w) for w in shape)
+        raise DdtError(f"{name} must have shape {want}, got {tuple(t.shape)}")
+    if contiguous and not t.is_contiguous():
+        raise DdtError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _q8_cache(c_kv, k_rope, scales, block_table, B) -> Q8Cache:
+    if not c_kv.is_cuda:
+        raise DdtError("c_kv must be a CUDA tensor")
+    dev, f8 = c_kv.device, torch.float8_e4m3fn
+    pages = c_kv.shape[0]
+    c = Q8Cache()
+    c.c_kv = _need(c_kv, "c_kv", f8, (None, PAGE_ROWS, D_LATENT), dev, contiguous=False)
+    c.k_rope = _need(k_rope, "k_rope", f8, (pages, PAGE_ROWS, D_ROPE), dev, contiguous=False)
+    if c_kv.stride(2) != 1 or k_rope.stride(2) != 1:
+        raise DdtError("cache rows must be contiguous in their last dimension")
+    c.scales = _need(scales, "scales", torch.float32, (pages,), dev)
+    c.block_table = _need(block_table, "block_table", torch.int32, (B, None), dev)
+    c.ckv_page_stride, c.ckv_row_stride = c_kv.stride(0), c_kv.stride(1)
+    c.kr_page_stride, c.kr_row_stride = k_rope.stride(0), k_rope.stride(1)
+    c.num_pages, c.max_blocks = pages, block_table.shape[1]
+    return c
+
+
+def kv_pages(prefix_lens: torch.Tensor, block_table: torch.Tensor, n_blocks: torch.Tensor,
+             free_pages: torch.Tensor, n_free: torch.Tensor, *, q_len: Optional[int] = None,
+             row_start: Optional[torch.Tensor] = None, n_rows: Optional[int] = None,
+             slots: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+             stream=None):
+    """Block tables and slot maps from the requests' lengths.  prefix_lens int32 [B];
+    block_table int32 [B, max_blocks], n_blocks int32 [B], free_pages int32
+    [num_pages] and n_free int32 [1] are updated in place.  Each request is to hold
+    q_len more rows, or row_start[b+1] - row_start[b] (int32 [B+1]; n_rows is then
+    the number of rows of all requests, unless slots tells it).  Returns (slots int64
+    [n_rows], status int32 [B])."""
+    if not prefix_lens.is_cuda:
+        raise DdtError("prefix_lens must be a CUDA tensor")
+    if (q_len is None) == (row_start is None):
+        raise DdtError("give either q_len or row_start")
+    dev, B = prefix_lens.device, prefix_lens.shape[0]
+    i32 = torch.int32
+    if q_len is not None:
+        if q_len < 0 or q_len >= 1 << 31:
+            raise DdtError(f"q_len must be a row count, got {q_len}")
+        if n_rows is not None and n_rows != B * q_len:
+            raise DdtError(f"n_rows must be B * q_len = {B * q_len}, got {n_rows}")
+        n_rows = B * q_len
+    elif n_rows is None:
+        if slots is None:
+            raise DdtError("row_start needs n_rows or slots")
+        n_rows = slots.shape[0]
+    p = (_need(prefix_lens, "prefix_lens", i32, (B,), dev),
+         _need(row_start, "row_start", i32, (B + 1,), dev))
+    state = (_need(block_table, "block_table", i32, (B, None), dev),
+             _need(n_blocks, "n_blocks", i32, (B,), dev),
+             _need(free_pages, "free_pages", i32, (None,), dev),
+             _need(n_free, "n_free", i32, (1,), dev))
+    slots = slots if slots is not None else torch.empty((n_rows,), dtype=torch.int64, device=dev)
+    status = status if status is not None else torch.empty((B,), dtype=i32, device=dev)
+    out = (_need(slots, "slots", torch.int64, (n_rows,), dev),
+           _need(status, "status", i32, (B,), dev))
+    with _OnDevice(dev, stream) as s:
+        _check(load().ddt_kv_pages(*p, B, q_len or 0, n_rows, free_pages.shape[0],
+                                   block_table.shape[1], *state, *out, s), "ddt_kv_pages")
+    return slots, status
+
+
+def kv_write_q8(c_kv: torch.Tensor, k_rope: torch.Tensor, scales: torch.Tensor,
+                block_table: torch.Tensor, prefix_lens: torch.Tensor, rows_ckv: torch.Tensor,
+                rows_krope: torch.Tensor, *, row_start: Optional[torch.Tensor] = None,
+                max_rows: Optional[int] = None, status: Optional[torch.Tensor] = None,
+                stream=None) -> torch.Tensor:
+    """bf16 rows quantised behind each request's prefix.  c_kv float8_e4m3fn [pages, 64,
+    512], k_rope float8_e4m3fn [pages, 64, 64] (pages and rows may be strided), scales
+    float32 [pages], block_table int32 [B, max_blocks].  rows_ckv [B, q_len, 512] and
+    rows_krope [B, q_len, 64]; or, with row_start int32 [B+1] and max_rows (no request
+    has more), [n_rows, 512] and [n_rows, 64].  Returns status int32 [B]."""
+    B = prefix_lens.shape[0]
+    c = _q8_cache(c_kv, k_rope, scales, block_table, B)
+    dev, i32, bf16 = c_kv.device, torch.int32, torch.bfloat16
+    if row_start is None:
+        if max_rows is not None:
+            raise DdtError("max_rows goes with row_start")
+        q = rows_ckv.shape[1]
+        n, max_rows = B * q, q
+        lat, rope = (B, q, D_LATENT), (B, q, D_ROPE)
+    else:
+        if max_rows is None:
+            raise DdtError("row_start needs max_rows")
+        n, q = rows_ckv.shape[0], 0
+        lat, rope = (n, D_LATENT), (n, D_ROPE)
+    status = status if status is not None else torch.empty((B,), dtype=i32, device=dev)
+    args = (_need(prefix_lens, "prefix_lens", i32, (B,), dev),
+            _need(row_start, "row_start", i32, (B + 1,), dev), B, q, int(max_rows), n,
+            _need(rows_ckv, "rows_ckv", bf16, lat, dev),
+            _need(rows_krope, "rows_krope", bf16, rope, dev),
+            _need(status, "status", i32, (B,), dev))
+    with _OnDevice(dev, stream) as s:
+        _check(load().ddt_kv_write_q8(ctypes.byref(c), *args, s), "ddt_kv_write_q8")
+    return status
+
+
+def _attn_q8_args(q_lat, q_rope, c_kv, k_rope, scales, block_table, prefix_lens, mask,
+                  softmax_scale, max_prefix, num_splits) -> AttnQ8Args:
+    B, Q, H, DL = q_lat.shape
+    dev = c_kv.device
+    a = AttnQ8Args()
+    a.B, a.q_len, a.num_heads, a.d_latent, a.d_rope = B, Q, H, DL, q_rope.shape[3]
+    a.cache = _q8_cache(c_kv, k_rope, scales, block_table, B)
+    a.q_lat = _need(q_lat, "q_lat", torch.bfloat16, (B, Q, H, DL), dev)
+    a.q_rope = _need(q_rope, "q_rope", torch.bfloat16, (B, Q, H, None), dev)
+    a.prefix_lens = _need(prefix_lens, "prefix_lens", torch.int32, (B,), dev)
+    a.mask = _need(mask, "mask", torch.int64, (B, Q, (Q + 63) // 64), dev)
+    a.softmax_scale = float(softmax_scale)
+    a.max_prefix, a.num_splits = int(max_prefix), int(num_splits)
+    return a
+
+
+def verify_attn_q8_workspace_size(q_lat, q_rope, c_kv, k_rope, scales, block_table, prefix_lens,
+                                  mask, softmax_scale, max_prefix: int,
+                                  num_splits: int = 0) -> tuple[int, int]:
+    """(workspace bytes, number of KV splits) the call will use."""
+    a = _attn_q8_args(q_lat, q_rope, c_kv, k_rope, scales, block_table, prefix_lens, mask,
+                      softmax_scale, max_prefix, num_splits)
+    lib = load()
+    with torch.cuda.device(c_kv.device):
+        return (int(lib.ddt_verify_attn_q8_workspace_size(ctypes.byref(a))),
+                int(lib.ddt_verify_attn_q8_num_splits(ctypes.byref(a))))
+
+
+def verify_attn_q8(q_lat: torch.Tensor, q_rope: torch.Tensor, c_kv: torch.Tensor,
+                   k_rope: torch.Tensor, scales: torch.Tensor, block_table: torch.Tensor,
+                   prefix_lens: torch.Tensor, mask: torch.Tensor, softmax_scale: float, *,
+                   max_prefix: int, out: Optional[torch.Tensor] = None,
+                   lse: Optional[torch.Tensor] = None, want_lse: bool = False,
+                   num_splits: int = 0, workspace: Optional[torch.Tensor] = None,
+                   status: Optional[torch.Tensor] = None, stream=None):
+    """Tree-verify MLA-absorb attention over the paged 8-bit cache (arguments of the cache
+    as for kv_write_q8, the others as for verify_attn).  q_len 1 with mask word 1 is a
+    plain decode step.  Returns (out bf16 [B, Q, 64, 512], lse float32 [B, Q, 64] or
+    None)."""
+    a = _attn_q8_args(q_lat, q_rope, c_kv, k_rope, scales, block_table, prefix_lens, mask,
+                      softmax_scale, max_prefix, num_splits)
+    B, Q, H, dev = a.B, a.q_len, a.num_heads, c_kv.device
+    if out is None:
+        out = torch.empty((B, Q, H, D_LATENT), dtype=torch.bfloat16, device=dev)
+    if lse is None and want_lse:
+        lse = torch.empty((B, Q, H), dtype=torch.float32, device=dev)
+    a.out = _need(out, "out", torch.bfloat16, (B, Q, H, D_LATENT), dev)
+    a.lse = _need(lse, "lse", torch.float32, (B, Q, H), dev)
+    a.status = _need(status, "status", torch.int32, (B,), dev)
+    lib = load()
+    with _OnDevice(dev, stream) as s:
+        if workspace is None:
+            need = int(lib.ddt_verify_attn_q8_workspace_size(ctypes.byref(a)))
+            if need:
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+                if stream is not None:  # freed when this returns, read until the call is done
+                    workspace.record_stream(stream)
+        if workspace is not None:
+            if workspace.device != dev:
+                raise DdtError(f"workspace must be on {dev}")
+            a.workspace = workspace.data_ptr()
+            a.workspace_bytes = workspace.numel() * workspace.element_size()
+        _check(lib.ddt_verify_attn_q8(ctypes.byref(a), s), "ddt_verify_attn_q8")
+    return out, lse
+
+
+def kv_compact_q8(c_kv: torch.Tensor, k_rope: torch.Tensor, scales: torch.Tensor,
+                  block_table: torch.Tensor, prefix_lens: torch.Tensor, path: torch.Tensor,
+                  accept_len: torch.Tensor, *, new_prefix_lens: Optional[torch.Tensor] = None,
+                  status: Optional[torch.Tensor] = None, stream=None):
+    """In-place compaction of the accepted rows in the paged 8-bit cache; pass
+    new_prefix_lens=prefix_lens to update the prefix lengths in place.  Returns
+    (new_prefix_lens, status)."""
+    B, Q = path.shape
+    c = _q8_cache(c_kv, k_rope, scales, block_table, B)
+    dev, i32 = c_kv.device, torch.int32
+    new = new_prefix_lens if new_prefix_lens is not None else torch.empty((B,), dtype=i32, device=dev)
+    status = status if status is not None else torch.empty((B,), dtype=i32, device=dev)
+    args = (_need(prefix_lens, "prefix_lens", i32, (B,), dev), _need(path, "path", i32, (B, Q), dev),
+            _need(accept_len, "accept_len", i32, (B,), dev), B, Q,
+            _need(new, "new_prefix_lens", i32, (B,), dev), _need(status, "status", i32, (B,), dev))
+    with _OnDevice(dev, stream) as s:
+        _check(load().ddt_kv_compact_q8(ctypes.byref(c), *args, s), "ddt_kv_compact_q8")
+    return new, status
 
 
 def selftest_bounded_wait(timeout_us: int = 2000, stream=None) -> torch.Tensor:
