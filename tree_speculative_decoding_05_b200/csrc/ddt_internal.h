@@ -92,6 +92,9 @@ cudaError_t launch_kv_compact_q8(const ddt_q8_cache& c, const int32_t* prefix_le
 ddt_status launch_verify_attn_q8(const ddt_attn_q8_args& a, int num_splits, float* part_o,
                                  float* part_lse, cudaStream_t stream);
 
+// The fault word of the paged kernel (see ddt_fault_flags).
+cudaError_t q8_fault_flags(uint32_t* flags, bool reset);
+
 int device_sm_count();
 
 // Sets the dynamic shared-memory limit of `func` once per CUDA context (`slot`

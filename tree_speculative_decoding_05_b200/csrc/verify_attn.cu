@@ -54,7 +54,6 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
-#include <mutex>
 
 #include "ddt.h"
 #include "ddt_internal.h"
@@ -64,6 +63,7 @@ __device__ unsigned int ddt_fault_word = 0;  // bit set, see ddt_fault_flags
 }  // namespace ddt
 
 #include "sm100_ptx.cuh"
+#include "verify_shared.cuh"
 
 namespace ddt {
 
@@ -204,14 +204,6 @@ struct VerifyParams {
   int split_base;      // partial index of this launch's split 0
 };
 
-// KV tile range [t0, t1) of split `split` for a cache of T rows.
-__host__ __device__ inline void split_range(int T, int num_splits, int split, int& t0, int& t1) {
-  const int n_tiles = (T + kVerifyTileKeys - 1) / kVerifyTileKeys;
-  const int per = (n_tiles + num_splits - 1) / num_splits;
-  t0 = split * per;
-  t1 = t0 + per < n_tiles ? t0 + per : n_tiles;
-}
-
 // One work item: a pair of tree nodes of one request over one KV split.
 struct WorkItem {
   int b, pair, split, P, T, end, t0, ntile, last_tile;  // end: last row + 1 of this pass
@@ -255,15 +247,6 @@ __device__ __forceinline__ WorkItem decode_item(const VerifyParams& p, int w, co
 // is masked, and rows below 0 (fewer than kTK rows) read as zeros.
 __device__ __forceinline__ int tile_start(const WorkItem& it, int t) {
   return t == it.last_tile ? it.end - va::kTK : va::kTK * t;
-}
-
-// The k-th work index of a cluster: rounds of n_clusters indices, alternating
-// direction ("snake"), so that with items sorted by decreasing cost each pair
-// gets a balanced mix (a static longest-first schedule).  -1 past the end.
-__device__ __forceinline__ int work_index(int k, int cluster, int n_clusters, int n_items) {
-  const int64_t w = static_cast<int64_t>(k) * n_clusters +
-                    ((k & 1) ? (n_clusters - 1 - cluster) : cluster);
-  return w < n_items ? static_cast<int>(w) : -1;
 }
 
 // Persistent kernel: each CTA pair (cluster of 2) loops over the work indices
@@ -946,45 +929,6 @@ __global__ void __launch_bounds__(256) verify_merge_kernel(const float* __restri
 // ---------------------------------------------------------------------------
 namespace {
 
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(ptr);
-  });
-  return fn;
-}
-
-// 3-D bf16 map: dims {d0 (contiguous), d1, d2}, byte strides of d1 and d2, box
-// {64, box1, 1}, 128-byte swizzle, zero fill out of bounds.
-bool make_map(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
-              uint64_t stride1_bytes, uint64_t stride2_bytes, uint32_t box1,
-              CUtensorMapDataType dtype = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, uint32_t box0 = 64) {
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return false;
-  const cuuint64_t dims[3] = {d0, d1, d2};
-  const cuuint64_t strides[2] = {stride1_bytes, stride2_bytes};
-  const cuuint32_t box[3] = {box0, box1, 1};
-  const cuuint32_t estride[3] = {1, 1, 1};
-  return fn(m, dtype, 3, const_cast<void*>(base), dims, strides, box, estride,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-}  // namespace
-
-namespace {
-
 // One launch of the verify kernel over key range `kv_mode` (see VerifyParams).
 ddt_status launch_pass(const ddt_attn_args& a, int kv_mode, int num_splits, int write_partials,
                        int split_base, float* part_o, float* part_lse, cudaStream_t stream) {
@@ -1112,7 +1056,9 @@ extern "C" ddt_status ddt_fault_flags(uint32_t* flags, int32_t reset) {
   if (!flags) return DDT_ERR_INVALID_ARG;
   unsigned int v = 0;
   if (cudaMemcpyFromSymbol(&v, ddt::ddt_fault_word, sizeof v) != cudaSuccess) return DDT_ERR_CUDA;
-  *flags = v;
+  uint32_t q8 = 0;
+  if (ddt::q8_fault_flags(&q8, reset != 0) != cudaSuccess) return DDT_ERR_CUDA;
+  *flags = v | q8;
   if (reset) {
     const unsigned int zero = 0;
     if (cudaMemcpyToSymbol(ddt::ddt_fault_word, &zero, sizeof zero) != cudaSuccess)

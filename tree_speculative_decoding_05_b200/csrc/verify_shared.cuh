@@ -1,0 +1,69 @@
+// verify_shared.cuh — what the two verify kernels (bf16 and paged 8-bit cache) have in
+// common: the split of a cache into tile ranges, the static schedule of work items over
+// CTA pairs, and the encoding of tensor maps.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <mutex>
+
+#include "ddt_internal.h"
+
+namespace ddt {
+
+// KV tile range [t0, t1) of split `split` for a cache of T rows.
+__host__ __device__ inline void split_range(int T, int num_splits, int split, int& t0, int& t1) {
+  const int n_tiles = (T + kVerifyTileKeys - 1) / kVerifyTileKeys;
+  const int per = (n_tiles + num_splits - 1) / num_splits;
+  t0 = split * per;
+  t1 = t0 + per < n_tiles ? t0 + per : n_tiles;
+}
+
+// The k-th work index of a cluster: rounds of n_clusters indices, alternating
+// direction ("snake"), so that with items sorted by decreasing cost each pair
+// gets a balanced mix (a static longest-first schedule).  -1 past the end.
+__device__ __forceinline__ int work_index(int k, int cluster, int n_clusters, int n_items) {
+  const int64_t w = static_cast<int64_t>(k) * n_clusters +
+                    ((k & 1) ? (n_clusters - 1 - cluster) : cluster);
+  return w < n_items ? static_cast<int>(w) : -1;
+}
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+inline EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(ptr);
+  });
+  return fn;
+}
+
+// 3-D map: dims {d0 (contiguous), d1, d2}, byte strides of d1 and d2, box {box0, box1,
+// 1}, 128-byte swizzle unless told otherwise, zero fill out of bounds.
+inline bool make_map(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
+                     uint64_t stride1_bytes, uint64_t stride2_bytes, uint32_t box1,
+                     CUtensorMapDataType dtype = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                     uint32_t box0 = 64, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {d0, d1, d2};
+  const cuuint64_t strides[2] = {stride1_bytes, stride2_bytes};
+  const cuuint32_t box[3] = {box0, box1, 1};
+  const cuuint32_t estride[3] = {1, 1, 1};
+  return fn(m, dtype, 3, const_cast<void*>(base), dims, strides, box, estride,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace ddt
