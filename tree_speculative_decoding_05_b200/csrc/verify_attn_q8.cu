@@ -34,10 +34,13 @@
 //     rows before the page's first with zeros and never reads those behind the sequence,
 //     which may hold anything.
 //   * TMEM per CTA: four S buffers (4 x 64 columns) + O (256 columns).
-//   * warps 0-3 softmax and epilogue; 4 and 8 fill the K rings of even and odd tiles, 6
-//     the V ring; 5, 10 issue S of even and odd tiles and 7 issues P V (on three
-//     sub-partitions); 9 checks a request's page numbers for its status; 11-14 split the
-//     next item's queries while this one's last tiles are at work.
+//   * warps 0-7 softmax and epilogue, two threads for each half row (32 keys each): with
+//     one, its 64 exponentials and splits outlast the MMAs of a tile (64 requests x 33
+//     nodes x 4096 rows: 1225 us, against 1098 us with two, back to back); 8 and 12 fill
+//     the K rings of even and odd tiles, 10 the V ring; 9, 14 issue S of even and odd
+//     tiles and 11 issues P V (on three sub-partitions); 13 checks a request's page
+//     numbers for its status; 15-18 split the next item's queries while this one's last
+//     tiles are at work.
 //   * S runs up to three tiles ahead of the softmax; O is rescaled only when the running
 //     maximum outgrows its reference by 2^2.75.
 //   * long caches: splits write normalised partials, merged by the bf16 call's merge.
@@ -64,11 +67,11 @@ namespace vq {
 constexpr int kPage = DDT_PAGE_ROWS;
 constexpr int kTK = 2 * kPage;  // keys per tile
 static_assert(kVerifyTileKeys % kTK == 0, "split ranges are whole tiles");
-constexpr int kWarpKProd0 = 4, kWarpSIss0 = 5, kWarpVProd = 6, kWarpPVIss = 7, kWarpKProd1 = 8,
-              kWarpStatus = 9, kWarpSIss1 = 10, kWarpQ0 = 11;
+constexpr int kWarpKProd0 = 8, kWarpSIss0 = 9, kWarpVProd = 10, kWarpPVIss = 11, kWarpKProd1 = 12,
+              kWarpStatus = 13, kWarpSIss1 = 14, kWarpQ0 = 15;
 constexpr int kQWarps = 4;
 constexpr int kThreads = 32 * (kWarpQ0 + kQWarps);
-constexpr int kSoftmaxThreads = 128;
+constexpr int kSoftmaxThreads = 256;
 constexpr int kBox = 8192;  // 64 rows x 128 bytes
 // Q: four latent chunks of 128 values hi, four lo, then rope hi and lo (64 x 64 bytes).
 constexpr int kQLo = 4 * kBox, kQRope = 8 * kBox, kQRopeLo = kQRope + kBox / 2;
@@ -87,8 +90,8 @@ constexpr int kOffKRing = kOffQ + kQBytes;
 constexpr int kOffVRing = kOffKRing + 2 * kKSlots * kKSlotBytes;
 constexpr int kOffP = kOffVRing + kVSlots * kBox;
 constexpr int kOffRedMax = kOffP + kPBufs * kPBufBytes;
-constexpr int kOffRedL = kOffRedMax + 2 * 128 * 4;
-constexpr int kOffQScale = kOffRedL + 128 * 4;  // float[kQSlots][64]
+constexpr int kOffRedL = kOffRedMax + 2 * 256 * 4;  // red_max: float[2][4][64]
+constexpr int kOffQScale = kOffRedL + 256 * 4;  // float[kQSlots][64]
 constexpr int kOffLen = kOffQScale + kQSlots * 64 * 4;
 constexpr int kOffOrder = kOffLen + kMaxSortedB * 4;
 constexpr int kOffBar = kOffOrder + kMaxSortedB * 4;
@@ -580,10 +583,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(vq::kThreads, 1)
     }
   } else {
     // -------------------------------------------------------- softmax warps
-    const int t = threadIdx.x;  // TMEM lane
-    const int m = t & 63;       // row within this CTA (head)
-    const int hf = t >> 6;      // which page of the tile / which half of each O columns
-    const uint32_t lane_addr = static_cast<uint32_t>(warp * 32) << 16;
+    const int t = threadIdx.x;
+    const int m = t & 63;         // row within this CTA (head)
+    const int hf = (t >> 6) & 1;  // which page of the tile / which half of each O columns
+    const int g = t >> 7;         // which 32 keys of the page, which half of O's chunks
+    // warp w reads TMEM lanes 32 (w % 4) on
+    const uint32_t lane_addr = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const int part_of = (2 * g + hf) * 64 + m;  // a row's four parts lie 64 apart
     const int W = (Q + 63) >> 6;
     const uint32_t p_full_leader0 = map_to_rank(bar(kBarP), 0);
     const uint32_t s_free_leader0 = map_to_rank(bar(kBarSFree), 0);
@@ -666,37 +672,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(vq::kThreads, 1)
         }
         mbar_wait(bar(kBarS + sbuf), static_cast<uint32_t>((G >> 2) & 1), abort_flag);
         tc_fence_after_sync();
-        float x[64];
+        float x[32];
         {
-          uint32_t r0[32], r1[32];
-          const uint32_t col = tmem + lane_addr + kTmemS + static_cast<uint32_t>(64 * sbuf);
-          tmem_ld32(col, r0);
-          tmem_ld32(col + 32u, r1);
+          uint32_t r0[32];
+          tmem_ld32(tmem + lane_addr + kTmemS + static_cast<uint32_t>(64 * sbuf + 32 * g), r0);
           tmem_wait_ld();
 #pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            x[c] = __uint_as_float(r0[c]);
-            x[32 + c] = __uint_as_float(r1[c]);
-          }
+          for (int c = 0; c < 32; ++c) x[c] = __uint_as_float(r0[c]);
         }
-        if (vis != ~0ull) {
-          const uint32_t v0 = static_cast<uint32_t>(vis), v1 = static_cast<uint32_t>(vis >> 32);
+        const uint32_t v32 = static_cast<uint32_t>(vis >> (32 * g));
+        if (v32 != ~0u) {
 #pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            if (!((v0 >> c) & 1u)) x[c] = -INFINITY;
-            if (!((v1 >> c) & 1u)) x[32 + c] = -INFINITY;
-          }
+          for (int c = 0; c < 32; ++c)
+            if (!((v32 >> c) & 1u)) x[c] = -INFINITY;
         }
         float mx = x[0];
 #pragma unroll
-        for (int c = 1; c < 64; ++c) mx = fmaxf(mx, x[c]);
+        for (int c = 1; c < 32; ++c) mx = fmaxf(mx, x[c]);
         tc_fence_before_sync();
         mx = fmaf(mx, sc, lk);  // a positive scale commutes with the maximum
-        red_max[sb * 128 + t] = mx;
+        float* const red = red_max + sb * 256;
+        red[part_of] = mx;
         named_barrier_sync(1, kSoftmaxThreads);
         // Every thread of this CTA has read S: release the buffer.
         if (t == 0) mbar_arrive_cluster(s_free_leader0 + 8u * sbuf);
-        mx = fmaxf(mx, red_max[sb * 128 + (t ^ 64)]);
+        mx = fmaxf(fmaxf(red[m], red[64 + m]), fmaxf(red[128 + m], red[192 + m]));
         float factor = 1.f;
         bool rescale = false;
         if (m_ref == -INFINITY) {
@@ -709,10 +709,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(vq::kThreads, 1)
         }
         m_use = m_ref == -INFINITY ? 0.f : m_ref;
         const float shift = lk - m_use + kBase;
-        uint32_t hi[16], lo[16];
+        uint32_t hi[8], lo[8];
         float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
+        for (int c = 0; c < 8; ++c) {
           uint16_t f[4];
 #pragma unroll
           for (int v = 0; v < 2; ++v) {
@@ -729,12 +729,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(vq::kThreads, 1)
         l_sum += ((part[0] + part[1]) + (part[2] + part[3])) * (1.f / ks);
         // The P buffer of this tile was last read by the P V of tile G - kPBufs.
         wait_o_through(G - kPBufs);
-        // P: K-major, 128-byte rows of 128 keys, swizzled; this thread's page is its
-        // half of the row.
+        // P: K-major, 128-byte rows of 128 keys, swizzled; this thread's keys are a
+        // quarter of the row.
         uint8_t* prow = base + kOffP + pbuf * kPBufBytes + m * 128;
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const int at = ((4 * hf + v) ^ (m & 7)) << 4;
+        for (int v = 0; v < 2; ++v) {
+          const int at = ((4 * hf + 2 * g + v) ^ (m & 7)) << 4;
           *reinterpret_cast<uint4*>(prow + at) =
               make_uint4(hi[4 * v], hi[4 * v + 1], hi[4 * v + 2], hi[4 * v + 3]);
           *reinterpret_cast<uint4*>(prow + kBox + at) =
@@ -743,7 +743,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(vq::kThreads, 1)
         if (jj > 0 && __any_sync(0xffffffffu, rescale)) {
           wait_o_through(G - 1);  // the P V of the previous tile is done
 #pragma unroll 1
-          for (int q = 0; q < 8; ++q) {
+          for (int q = 4 * g; q < 4 * g + 4; ++q) {
             uint32_t o[32];
             const uint32_t addr = tmem + lane_addr + kTmemO + 32u * q;
             tmem_ld32(addr, o);
@@ -761,9 +761,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(vq::kThreads, 1)
       }
       // ----------------------------------------------------------- epilogue
       wait_o_through(G - 1);
-      red_l[t] = l_sum;
+      red_l[part_of] = l_sum;
       named_barrier_sync(1, kSoftmaxThreads);
-      const float l_row = l_sum + red_l[t ^ 64];
+      const float l_row = (red_l[m] + red_l[64 + m]) + (red_l[128 + m] + red_l[192 + m]);
       const bool empty_row = l_row == 0.f;
       const float inv = empty_row ? 0.f : 1.f / l_row;
       const float lse_nat = empty_row ? -INFINITY : (m_use - kBase + __log2f(l_row)) * kLn2;
@@ -779,7 +779,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(vq::kThreads, 1)
 #pragma unroll 1
         for (int nh = 0; nh < 2; ++nh) {
 #pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
+          for (int q = 2 * g; q < 2 * g + 2; ++q) {
             uint32_t o[32];
             tmem_ld32(tmem + lane_addr + kTmemO + 128u * nh + 32u * q, o);
             tmem_wait_ld();
@@ -808,25 +808,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(vq::kThreads, 1)
           }
           named_barrier_sync(2, kSoftmaxThreads);
         }
-        if (hf == 0 && p.lse) p.lse[static_cast<int64_t>(row0) + m] = lse_nat;
+        if (t < 64 && p.lse) p.lse[static_cast<int64_t>(row0) + m] = lse_nat;
       } else {
         // A split's normalised fp32 partial, in four rounds of 64 rows x 128 columns.
         const int64_t rows_total = static_cast<int64_t>(p.B) * Q * 64;
         const int64_t row0 = split * rows_total + (static_cast<int64_t>(b) * Q + node) * 64;
 #pragma unroll 1
         for (int r = 0; r < 4; ++r) {
-#pragma unroll 1
-          for (int qq = 0; qq < 2; ++qq) {
-            uint32_t o[32];
-            tmem_ld32(tmem + lane_addr + kTmemO + 128u * (r >> 1) + 32u * (2 * (r & 1) + qq), o);
-            tmem_wait_ld();
-            uint8_t* rowp = stage + (2 * hf + qq) * kBox + m * 128;
+          uint32_t o[32];
+          tmem_ld32(tmem + lane_addr + kTmemO + 128u * (r >> 1) + 32u * (2 * (r & 1) + g), o);
+          tmem_wait_ld();
+          uint8_t* rowp = stage + (2 * hf + g) * kBox + m * 128;
 #pragma unroll
-            for (int v = 0; v < 8; ++v)
-              *reinterpret_cast<float4*>(rowp + ((v ^ (m & 7)) << 4)) =
-                  make_float4(__uint_as_float(o[4 * v]) * inv, __uint_as_float(o[4 * v + 1]) * inv,
-                              __uint_as_float(o[4 * v + 2]) * inv, __uint_as_float(o[4 * v + 3]) * inv);
-          }
+          for (int v = 0; v < 8; ++v)
+            *reinterpret_cast<float4*>(rowp + ((v ^ (m & 7)) << 4)) =
+                make_float4(__uint_as_float(o[4 * v]) * inv, __uint_as_float(o[4 * v + 1]) * inv,
+                            __uint_as_float(o[4 * v + 2]) * inv, __uint_as_float(o[4 * v + 3]) * inv);
           if (r == 3) tc_fence_before_sync();
           fence_proxy_async_smem();
           named_barrier_sync(2, kSoftmaxThreads);
@@ -841,7 +838,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(vq::kThreads, 1)
           }
           named_barrier_sync(2, kSoftmaxThreads);
         }
-        if (hf == 0) p.part_lse[row0 + m] = lse_nat;
+        if (t < 64) p.part_lse[row0 + m] = lse_nat;
       }
     }
     if (t == 0) bulk_wait_group0();  // this CTA's output stores have completed
