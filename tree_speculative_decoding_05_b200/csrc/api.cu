@@ -42,8 +42,8 @@ bool q8_cache_ok(const ddt_q8_cache& c) {
   if (!aligned16(c.c_kv) || !aligned16(c.k_rope)) return false;
   if ((c.ckv_page_stride | c.ckv_row_stride | c.kr_page_stride | c.kr_row_stride) % 16) return false;
   if (c.ckv_row_stride < DDT_D_LATENT || c.kr_row_stride < DDT_D_ROPE) return false;
-  // tensor maps take strides below 2^40 bytes
-  if (c.ckv_row_stride >= (int64_t{1} << 33) || c.kr_row_stride >= (int64_t{1} << 33)) return false;
+  // tensor maps take strides below 2^40 bytes; rows are addressed within their page
+  if (c.ckv_row_stride > INT32_MAX || c.kr_row_stride > INT32_MAX) return false;
   if (c.ckv_page_stride >= (int64_t{1} << 40) || c.kr_page_stride >= (int64_t{1} << 40)) return false;
   return c.num_pages == 1 || (c.ckv_page_stride >= DDT_PAGE_ROWS * c.ckv_row_stride &&
                               c.kr_page_stride >= DDT_PAGE_ROWS * c.kr_row_stride);

@@ -19,6 +19,7 @@
 
 #include "ddt.h"
 #include "ddt_internal.h"
+#include "q8_common.cuh"
 
 namespace ddt {
 
@@ -51,15 +52,32 @@ __device__ __forceinline__ Span load_span(const int32_t* prefix_lens, const int3
   return s;
 }
 
+// Cluster barrier in two halves: what a CTA wrote (or read) before its arrival lies
+// before what any CTA does after its wait.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ int cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return static_cast<int>(r);
+}
+
 // ---------------------------------------------------------------------------
 // Page plan.  The state (tables, counts, the stack) is small and every request's
-// place on the stack depends on all requests before it, so one CTA scans the
-// requests, 1024 at a time, and moves the page numbers; nothing depends on the
-// order in which threads run.  Latency-bound: a handful of dependent loads, two
-// block scans and the page numbers themselves.
+// place on the stack depends on all requests before it, so each CTA scans the
+// requests for itself, 1024 at a time, and the CTAs of one cluster share the page
+// numbers to be moved and the slots; nothing depends on the order in which threads
+// run.  Latency-bound: a handful of dependent loads, two block scans and the page
+// numbers themselves.
 // ---------------------------------------------------------------------------
 constexpr int kPlanThreads = 1024;
+constexpr int kPlanCtas = 8;  // of a large plan
 constexpr int kSlotThreads = 256;
+constexpr int kSlotRows = 4 * kSlotThreads;  // rows of one CTA at a time
 
 // Inclusive scan over the CTA; `total` is the sum.  s_warp: 33 entries.
 __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* s_warp, int64_t& total) {
@@ -98,36 +116,41 @@ __device__ __forceinline__ int64_t slot_of(const Span& s, int64_t i, int n_block
   return page < 0 || page >= num_pages ? -1 : static_cast<int64_t>(page) * kPage + pos % kPage;
 }
 
-// Slots of rows [r0, r0 + step, ...) below n_rows (all -1 with `refused`); each row's
-// request by bisection.
+// Slots of rows [r0, r1) (all -1 with `refused`), row r0 + t + i * threads by thread t.
+// A row's request is found by bisection, unless it is that of the thread's row before.
 __device__ void write_slots(bool refused, const int32_t* prefix_lens, const int32_t* row_start,
-                            int B, int q_len, int64_t n_rows, int num_pages, int max_blocks,
+                            int B, int q_len, int64_t r0, int64_t r1, int num_pages, int max_blocks,
                             const int32_t* block_table, const int32_t* n_blocks, int64_t* slots,
-                            int64_t r0, int64_t step) {
-  for (int64_t r = r0; r < n_rows; r += step) {
-    int b;
+                            int t, int threads) {
+  if (!row_start && q_len == 0) return;
+  int b = 0;
+  for (int64_t r = r0 + t; r < r1; r += threads) {
     if (row_start) {
-      int lo = 0, hi = B;  // the last request with row_start[b] <= r
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (row_start[mid] <= r) lo = mid;
-        else hi = mid;
+      if (row_start[b + 1] <= r) {
+        int hi = B;  // the last request with row_start[b] <= r
+        while (hi - b > 1) {
+          const int mid = (b + hi) >> 1;
+          if (row_start[mid] <= r) b = mid;
+          else hi = mid;
+        }
       }
-      b = lo;
     } else {
-      if (q_len == 0 || r / q_len >= B) return;
-      b = static_cast<int>(r / q_len);
+      if (r >= static_cast<int64_t>(B) * q_len) return;
+      b = r <= UINT_MAX ? static_cast<int>(static_cast<uint32_t>(r) / static_cast<uint32_t>(q_len))
+                        : static_cast<int>(r / q_len);
     }
     const Span s = load_span(prefix_lens, row_start, b, q_len, max_blocks);
     const int64_t i = r - s.first;
-    if (i < 0) continue;
-    if (row_start && i >= static_cast<int64_t>(row_start[b + 1]) - s.first) continue;
+    if (i < 0 || (row_start && r >= row_start[b + 1])) continue;  // no request's row
     slots[r] = refused ? -1
                        : slot_of(s, i, n_blocks[b], num_pages, max_blocks,
                                  block_table + static_cast<int64_t>(b) * max_blocks);
   }
 }
 
+// kCtas CTAs in one cluster (or one alone).  Every CTA derives the same plan from the
+// state as it was; the state is changed only behind a cluster barrier.
+template <int kCtas>
 __global__ void __launch_bounds__(kPlanThreads) kv_pages_kernel(
     const int32_t* __restrict__ prefix_lens, const int32_t* __restrict__ row_start, int B,
     int q_len, int64_t slot_rows, int num_pages, int max_blocks, int32_t* block_table,
@@ -136,7 +159,16 @@ __global__ void __launch_bounds__(kPlanThreads) kv_pages_kernel(
   __shared__ int64_t s_upto[kPlanThreads];  // pages of the chunk's requests up to and with each
   __shared__ int s_from[kPlanThreads];      // table entry at which a request's pages begin
   const int t = threadIdx.x;
+  const int rank = kCtas > 1 ? cluster_rank() : 0;
   const bool one_chunk = B <= kPlanThreads;
+  auto barrier = [] {  // all CTAs have come here; memory as the others left it
+    if constexpr (kCtas > 1) {
+      cluster_arrive();
+      cluster_wait();
+    } else {
+      __syncthreads();
+    }
+  };
 
   struct Request {
     int held, need, status;
@@ -148,11 +180,12 @@ __global__ void __launch_bounds__(kPlanThreads) kv_pages_kernel(
     q.held = n_blocks[b];
     q.status = s.status;
     if (q.status == DDT_REQ_OK && (q.held < 0 || q.held > max_blocks)) q.status = DDT_REQ_BAD_INDEX;
-    q.need = (s.prefix + s.rows + kPage - 1) / kPage;  // <= max_blocks when the status is OK
-    if (q.status != DDT_REQ_OK) q.held = q.need = 0;   // neither gives nor takes
+    if (q.status != DDT_REQ_OK) q.held = 0;  // neither gives nor takes
+    else q.need = (s.prefix + s.rows + kPage - 1) / kPage;
   };
-  // Runs over the chunk's moving pages, all threads together: `amount` pages of each
-  // thread's request, from table entry `from` on; f(request, table entry, place).
+  // Runs over the chunk's moving pages, the threads of all CTAs together: `amount`
+  // pages of each thread's request, from table entry `from` on; f(request, table entry,
+  // place).
   auto move_pages = [&](int b0, int amount, int from, auto f) -> int64_t {
     int64_t total;
     const int64_t upto = block_scan(amount, s_warp, total);
@@ -160,7 +193,8 @@ __global__ void __launch_bounds__(kPlanThreads) kv_pages_kernel(
     s_upto[t] = upto;
     s_from[t] = from;
     __syncthreads();
-    for (int64_t k = t; k < total; k += kPlanThreads) {
+    for (int64_t k = static_cast<int64_t>(rank) * kPlanThreads + t; k < total;
+         k += kCtas * kPlanThreads) {
       int lo = 0, hi = kPlanThreads - 1;  // first request with s_upto > k
       while (lo < hi) {
         const int mid = (lo + hi) >> 1;
@@ -187,16 +221,9 @@ __global__ void __launch_bounds__(kPlanThreads) kv_pages_kernel(
     }
   }
   const int64_t free1 = free0 + back;
-  if (free0 < 0 || free1 > num_pages) {  // no such state: change nothing
-    for (int b = t; b < B; b += kPlanThreads)
-      if (status) status[b] = DDT_REQ_BAD_INDEX;
-    if (slots)
-      write_slots(true, prefix_lens, row_start, B, q_len, slot_rows, num_pages, max_blocks,
-                  block_table, n_blocks, slots, t, kPlanThreads);
-    return;
-  }
+  const bool refused = free0 < 0 || free1 > num_pages;  // no such state: change nothing
   // 2. they go onto the stack, the first request's first page on top
-  if (back > 0) {
+  if (back > 0 && !refused) {
     int64_t done = 0;
     for (int b0 = 0; b0 < B; b0 += kPlanThreads) {
       if (!one_chunk) load(b0 + t);
@@ -207,14 +234,15 @@ __global__ void __launch_bounds__(kPlanThreads) kv_pages_kernel(
         *e = -1;
       });
     }
+    barrier();
   }
   // 3. pages are taken from the top, request by request
   int64_t wanted = 0, taken = 0;
   for (int b0 = 0; b0 < B; b0 += kPlanThreads) {
     if (!one_chunk) load(b0 + t);
     const int mine = q.need > q.held ? q.need - q.held : 0;
-    int st = q.status;
-    if (__syncthreads_or(mine)) {
+    int st = refused ? DDT_REQ_BAD_INDEX : q.status;
+    if (__syncthreads_or(mine) && !refused) {
       int64_t total;
       const int64_t upto = wanted + block_scan(mine, s_warp, total);
       const bool served = upto <= free1;
@@ -227,18 +255,22 @@ __global__ void __launch_bounds__(kPlanThreads) kv_pages_kernel(
       });
       wanted += total;
     }
+    if constexpr (kCtas > 1) barrier();  // every CTA has read this chunk's counts
     const int b = b0 + t;
-    if (b < B) {
+    if (b < B && rank == 0) {
       if (st == DDT_REQ_OK && q.need != q.held) n_blocks[b] = q.need;
       if (status) status[b] = st;
     }
   }
-  if (t == 0 && free1 - taken != free0) *n_free = static_cast<int>(free1 - taken);
-  // 4. few rows: their slots too
+  if (rank == 0 && t == 0 && !refused && free1 - taken != free0)
+    *n_free = static_cast<int>(free1 - taken);
+  // 4. not too many rows: their slots too
   if (slots && slot_rows > 0) {
-    __syncthreads();
-    write_slots(false, prefix_lens, row_start, B, q_len, slot_rows, num_pages, max_blocks,
-                block_table, n_blocks, slots, t, kPlanThreads);
+    barrier();
+    const int64_t per = (slot_rows + kCtas - 1) / kCtas, r0 = rank * per;
+    write_slots(refused, prefix_lens, row_start, B, q_len, r0,
+                r0 + per < slot_rows ? r0 + per : slot_rows, num_pages, max_blocks, block_table,
+                n_blocks, slots, t, kPlanThreads);
   }
 }
 
@@ -257,27 +289,16 @@ __global__ void __launch_bounds__(kSlotThreads) kv_slots_kernel(
                held > (s.prefix + s.rows + kPage - 1) / kPage;
   }
   refused = __syncthreads_or(refused);
-  write_slots(refused, prefix_lens, row_start, B, q_len, n_rows, num_pages, max_blocks,
-              block_table, n_blocks, slots,
-              static_cast<int64_t>(blockIdx.x) * kSlotThreads + threadIdx.x,
-              static_cast<int64_t>(gridDim.x) * kSlotThreads);
+  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * kSlotRows; r0 < n_rows;
+       r0 += static_cast<int64_t>(gridDim.x) * kSlotRows)
+    write_slots(refused, prefix_lens, row_start, B, q_len, r0,
+                r0 + kSlotRows < n_rows ? r0 + kSlotRows : n_rows, num_pages, max_blocks,
+                block_table, n_blocks, slots, threadIdx.x, kSlotThreads);
 }
 
 // ---------------------------------------------------------------------------
 // e4m3
 // ---------------------------------------------------------------------------
-// Smallest power of two >= 2^kMinExp with amax <= 448 * scale, for the bits of a
-// finite bf16 magnitude: 448 = 1.75 * 2^8, so the exponent is amax's less 8, one
-// more when amax's significand exceeds 1.75.
-__device__ __forceinline__ int fit_exponent(uint32_t amax_bits) {
-  const int e = static_cast<int>(amax_bits >> 7) - 127 - 8 + ((amax_bits & 0x7fu) > 0x60u);
-  return e < kMinExp ? kMinExp : e;
-}
-
-__device__ __forceinline__ float pow2f(int e) {  // -126 <= e <= 127
-  return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-}
-
 __device__ __forceinline__ bool scale_ok(float s) { return s > 0.f && s <= 3.402823466e38f; }
 
 // Two floats to two e4m3 bytes (round to nearest even, saturating, NaN kept).
@@ -297,14 +318,15 @@ __device__ __forceinline__ uint4 rescale16(uint4 v, float ratio) {
                     rescale4(v.w, ratio));
 }
 
-// Address of 16-byte vector v (latent, then rope) of row r of a page.
-__device__ __forceinline__ uint4* row_vec(const ddt_q8_cache& c, int64_t page, int r, int v) {
-  uint8_t* p = v < kLatVec8
-                   ? static_cast<uint8_t*>(c.c_kv) + page * c.ckv_page_stride + r * c.ckv_row_stride +
-                         16 * v
-                   : static_cast<uint8_t*>(c.k_rope) + page * c.kr_page_stride +
-                         r * c.kr_row_stride + 16 * (v - kLatVec8);
-  return reinterpret_cast<uint4*>(p);
+// Address of vector v (16 bytes; latent, then rope) of row 0 of a page, and the distance
+// of the rows there (host-checked to fit).
+__device__ __forceinline__ uint8_t* page_vec(const ddt_q8_cache& c, int64_t page, int v) {
+  return v < kLatVec8 ? static_cast<uint8_t*>(c.c_kv) + page * c.ckv_page_stride + 16 * v
+                      : static_cast<uint8_t*>(c.k_rope) + page * c.kr_page_stride +
+                            16 * (v - kLatVec8);
+}
+__device__ __forceinline__ int row_step(const ddt_q8_cache& c, int v) {
+  return static_cast<int>(v < kLatVec8 ? c.ckv_row_stride : c.kr_row_stride);
 }
 
 // ---------------------------------------------------------------------------
@@ -315,70 +337,56 @@ __device__ __forceinline__ uint4* row_vec(const ddt_q8_cache& c, int64_t page, i
 // latency of load, reduction and store for a step's rows.  Pages that only get
 // rows of their own request need no other CTA's result.
 // ---------------------------------------------------------------------------
-constexpr int kWriteThreads = 256;
-constexpr int kVecPerThread = kPage * kRowVec16 / kWriteThreads;  // 18
-static_assert(kVecPerThread * kWriteThreads == kPage * kRowVec16, "a page is whole rounds");
+// The CTAs of a request that reaches few pages (kCluster, at most kMaxWriteCluster) are
+// one cluster: the first one sets the status before the cluster's barrier, the others
+// raise it behind it if they met a value that is not finite.  Those of a long prompt
+// raise a status that was cleared before the launch.
+constexpr int kWriteThreads = 512;
+constexpr int kLatRows = kWriteThreads / kLatVec16;   // latent rows of one round (8)
+constexpr int kLatPerThread = kPage / kLatRows;       // 8
+constexpr int kVecPerThread = kLatPerThread + 1;
+static_assert(kWriteThreads == kPage * (kRowVec16 - kLatVec16), "one rope vector per thread");
+constexpr int kMaxWriteCluster = 4;
 
-__global__ void __launch_bounds__(kWriteThreads) kv_write_q8_kernel(
-    const ddt_q8_cache c, const int32_t* __restrict__ prefix_lens,
-    const int32_t* __restrict__ row_start, int q_len, int max_rows, int64_t n_rows,
-    const uint16_t* __restrict__ rows_ckv, const uint16_t* __restrict__ rows_krope,
-    int32_t* __restrict__ status, int pages_per_request) {
-  __shared__ uint32_t s_max[kWriteThreads / 32];
-  const int b = blockIdx.x / pages_per_request;
-  const int k = blockIdx.x % pages_per_request;
-  const int t = threadIdx.x;
-  Span s = load_span(prefix_lens, row_start, b, q_len, c.max_blocks);
-  if (s.status == DDT_REQ_OK && (s.rows > max_rows || s.first + s.rows > n_rows))
-    s.status = DDT_REQ_BAD_LENGTH;
-  // Every page of the request's rows has to be one before any is written.
-  const int blk0 = s.prefix / kPage;
-  const int32_t* table = c.block_table + static_cast<int64_t>(b) * c.max_blocks;
-  int bad = 0;
-  if (s.status == DDT_REQ_OK && s.rows > 0) {
-    const int last = (s.prefix + s.rows - 1) / kPage;
-    for (int blk = blk0 + t; blk <= last; blk += kWriteThreads) {
-      const int page = table[blk];
-      bad |= page < 0 || page >= c.num_pages;
-    }
-  }
-  if (__syncthreads_or(bad)) s.status = DDT_REQ_BAD_INDEX;
-  if (s.status != DDT_REQ_OK) {
-    if (k == 0 && t == 0 && status) status[b] = s.status;
-    return;
-  }
-  // This page's rows: cache rows [lo, hi).
-  const int64_t page0 = static_cast<int64_t>(blk0 + k) * kPage;
-  const int64_t lo = k == 0 ? s.prefix : page0;
-  const int64_t end = static_cast<int64_t>(s.prefix) + s.rows;
-  const int64_t hi = end < page0 + kPage ? end : page0 + kPage;
-  if (lo >= hi) return;
-  const int page = table[blk0 + k];
-  const int off = static_cast<int>(lo - page0);
-  const int n = static_cast<int>(hi - lo);
-  const int64_t src = s.first + (lo - s.prefix);
-  const float old_scale = c.scales[page];
-
-  const uint4* lat = reinterpret_cast<const uint4*>(rows_ckv) + src * kLatVec16;
-  const uint4* rope = reinterpret_cast<const uint4*>(rows_krope) + src * (kRowVec16 - kLatVec16);
+// Vectors of the page's new rows that a thread holds: eight of latent values, vector
+// t % 64 of rows t / 64 + 8 i, so that a thread's addresses lie one distance apart, and
+// one of rope values, vector t % 8 of row t / 8.
+struct PageRows {
   uint4 x[kVecPerThread];
+};
+
+__device__ __forceinline__ void load_page_rows(PageRows& p, int64_t src, int n,
+                                               const uint16_t* rows_ckv,
+                                               const uint16_t* rows_krope) {
+  const int t = threadIdx.x;
+  const uint4* lat = reinterpret_cast<const uint4*>(rows_ckv) + src * kLatVec16 + t;
+  const uint4* rope = reinterpret_cast<const uint4*>(rows_krope) + src * (kRowVec16 - kLatVec16) + t;
 #pragma unroll
-  for (int i = 0; i < kVecPerThread; ++i) {
-    const int idx = t + i * kWriteThreads, r = idx / kRowVec16, v = idx - r * kRowVec16;
-    x[i] = make_uint4(0, 0, 0, 0);
-    if (r < n) x[i] = v < kLatVec16 ? lat[r * kLatVec16 + v]
-                                    : rope[r * (kRowVec16 - kLatVec16) + v - kLatVec16];
+  for (int i = 0; i < kLatPerThread; ++i) {
+    p.x[i] = make_uint4(0, 0, 0, 0);
+    if (t / kLatVec16 + i * kLatRows < n) p.x[i] = lat[i * kWriteThreads];
   }
-  // Largest magnitude as bf16 bits, two lanes at a time.
+  p.x[kLatPerThread] = make_uint4(0, 0, 0, 0);
+  if (t / (kRowVec16 - kLatVec16) < n) p.x[kLatPerThread] = *rope;
+}
+
+// The n rows to page rows off .. off + n - 1, by the whole CTA; returns whether a value
+// was not finite.
+__device__ __forceinline__ int write_page(const ddt_q8_cache& c, PageRows& rows, int page, int off,
+                                          int n, uint32_t* s_max) {
+  uint4 (&x)[kVecPerThread] = rows.x;
+  const int t = threadIdx.x;
+  const float old_scale = c.scales[page];
+  // Largest magnitude as bf16 bits, two at a time (NaN when there is one).
   uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < kVecPerThread; ++i) {
-    m = __vmaxu2(m, x[i].x & 0x7fff7fffu);
-    m = __vmaxu2(m, x[i].y & 0x7fff7fffu);
-    m = __vmaxu2(m, x[i].z & 0x7fff7fffu);
-    m = __vmaxu2(m, x[i].w & 0x7fff7fffu);
+    m = max_abs_bf16x2(m, x[i].x);
+    m = max_abs_bf16x2(m, x[i].y);
+    m = max_abs_bf16x2(m, x[i].z);
+    m = max_abs_bf16x2(m, x[i].w);
   }
-  uint32_t top = max(m & 0xffffu, m >> 16);
+  uint32_t top = max_of_halves(m);
   // Not a finite value among them: NaN becomes 0, an infinity the largest finite
   // bf16 (which saturates), and the maximum is taken again over finite values.
   const bool odd = top >= 0x7f80u;
@@ -404,7 +412,7 @@ __global__ void __launch_bounds__(kWriteThreads) kv_write_q8_kernel(
   const int any_odd = __syncthreads_or(odd);
 #pragma unroll
   for (int i = 0; i < kWriteThreads / 32; ++i) top = max(top, s_max[i]);
-  const int e = fit_exponent(top);
+  const int fit = e4m3_exponent(top), e = fit < kMinExp ? kMinExp : fit;
   float scale = pow2f(e), inv = pow2f(-e);
   if (off > 0 && scale_ok(old_scale) && old_scale >= scale) {
     scale = old_scale;
@@ -413,37 +421,96 @@ __global__ void __launch_bounds__(kWriteThreads) kv_write_q8_kernel(
     // The live rows before these move to the larger scale.
     const float ratio = scale_ok(old_scale) ? old_scale * inv : 0.f;
     for (int idx = t; idx < off * kRowVec8; idx += kWriteThreads) {
-      uint4* p = row_vec(c, page, idx / kRowVec8, idx % kRowVec8);
+      const int r = idx / kRowVec8, v = idx - r * kRowVec8;
+      uint4* p = reinterpret_cast<uint4*>(page_vec(c, page, v) + static_cast<int64_t>(r) * row_step(c, v));
       *p = rescale16(*p, ratio);
     }
   }
-#pragma unroll
-  for (int i = 0; i < kVecPerThread; ++i) {
-    const int idx = t + i * kWriteThreads, r = idx / kRowVec16, v = idx - r * kRowVec16;
-    if (r >= n) continue;
-    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+  // bf16 vector v holds half of e4m3 vector v / 2
+  auto store = [&](const uint4& a, uint8_t* at) {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
     uint32_t h[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       h[j] = to_e4m3x2(__uint_as_float(w[j] << 16) * inv, __uint_as_float(w[j] & 0xffff0000u) * inv);
-    const uint2 y = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
-    // bf16 vector v holds half an e4m3 vector
-    reinterpret_cast<uint2*>(row_vec(c, page, off + r, v >> 1))[v & 1] = y;
+    *reinterpret_cast<uint2*>(at) = make_uint2(__byte_perm(h[0], h[1], 0x5410), __byte_perm(h[2], h[3], 0x5410));
+  };
+  const int lat_step = row_step(c, 0);
+  uint8_t* lat = page_vec(c, page, 0) + 8 * (t % kLatVec16) +
+                 static_cast<int64_t>(off + t / kLatVec16) * lat_step;
+#pragma unroll
+  for (int i = 0; i < kLatPerThread; ++i)
+    if (t / kLatVec16 + i * kLatRows < n) store(x[i], lat + static_cast<int64_t>(i * kLatRows) * lat_step);
+  constexpr int kRopeVec16 = kRowVec16 - kLatVec16;
+  if (t / kRopeVec16 < n)
+    store(x[kLatPerThread], page_vec(c, page, kLatVec8) + 8 * (t % kRopeVec16) +
+                                static_cast<int64_t>(off + t / kRopeVec16) * row_step(c, kLatVec8));
+  if (t == 0 && scale != old_scale) c.scales[page] = scale;
+  return any_odd;
+}
+
+template <bool kCluster>
+__global__ void __launch_bounds__(kWriteThreads, 1024 / kWriteThreads) kv_write_q8_kernel(
+    const ddt_q8_cache c, const int32_t* __restrict__ prefix_lens,
+    const int32_t* __restrict__ row_start, int q_len, int max_rows, int64_t n_rows,
+    const uint16_t* __restrict__ rows_ckv, const uint16_t* __restrict__ rows_krope,
+    int32_t* __restrict__ status, int pages_per_request) {
+  __shared__ uint32_t s_max[kWriteThreads / 32];
+  const int b = blockIdx.x / pages_per_request;
+  const int k = blockIdx.x % pages_per_request;
+  const int t = threadIdx.x;
+  Span s = load_span(prefix_lens, row_start, b, q_len, c.max_blocks);
+  if (s.status == DDT_REQ_OK && (s.rows > max_rows || s.first + s.rows > n_rows))
+    s.status = DDT_REQ_BAD_LENGTH;
+  const int blk0 = s.prefix / kPage;
+  // This page's rows: cache rows [lo, hi).
+  const int64_t page0 = static_cast<int64_t>(blk0 + k) * kPage;
+  const int64_t lo = k == 0 ? s.prefix : page0;
+  const int64_t end = static_cast<int64_t>(s.prefix) + s.rows;
+  const int64_t hi = end < page0 + kPage ? end : page0 + kPage;
+  if (!kCluster && k > 0 && lo >= hi) return;
+  // The rows are on their way while the page numbers are looked at: every page of the
+  // request's rows has to be one before any is written.
+  PageRows rows;
+  const int n = s.status == DDT_REQ_OK && lo < hi ? static_cast<int>(hi - lo) : 0;
+  load_page_rows(rows, s.first + (lo - s.prefix), n, rows_ckv, rows_krope);
+  const int32_t* table = c.block_table + static_cast<int64_t>(b) * c.max_blocks;
+  int bad = 0;
+  if (s.status == DDT_REQ_OK && s.rows > 0) {
+    const int last = (s.prefix + s.rows - 1) / kPage;
+    for (int blk = blk0 + t; blk <= last; blk += kWriteThreads) {
+      const int page = table[blk];
+      bad |= page < 0 || page >= c.num_pages;
+    }
   }
-  if (t == 0) {
-    if (scale != old_scale) c.scales[page] = scale;
-    if (any_odd && status) atomicMax(&status[b], DDT_REQ_NOT_FINITE);
+  if (__syncthreads_or(bad)) s.status = DDT_REQ_BAD_INDEX;
+  if (s.status != DDT_REQ_OK) {
+    if (k == 0 && t == 0 && status) status[b] = s.status;
+    return;
   }
+  int any_odd = 0;
+  if (n > 0) any_odd = write_page(c, rows, table[blk0 + k], static_cast<int>(lo - page0), n, s_max);
+  if (!status) return;
+  if (t == 0 && k == 0 && (kCluster || pages_per_request == 1))
+    status[b] = any_odd ? DDT_REQ_NOT_FINITE : DDT_REQ_OK;
+  if constexpr (kCluster) {
+    cluster_arrive();
+    cluster_wait();
+  }
+  if (t == 0 && k > 0 && any_odd) atomicMax(&status[b], DDT_REQ_NOT_FINITE);
+  if (t == 0 && k == 0 && !kCluster && pages_per_request > 1 && any_odd)
+    atomicMax(&status[b], DDT_REQ_NOT_FINITE);
 }
 
 // ---------------------------------------------------------------------------
-// Compaction.  One CTA per request: the moving rows (576 bytes each, at most 72
-// KB) are all read into shared memory before any byte is written, so the gather
-// is race-free for any path.  The scales of the at most three pages that rows
-// move into are known from the pages' present scales alone, without a look at the
-// values: a scale only ever rises, to the largest among the rows that come in.
+// Compaction.  One CTA per request: the moving rows (576 bytes each, at most 72 KB) are
+// all read into shared memory before any byte is written, so the gather is race-free
+// for any path.  The scales of the at most three pages that rows move into are known
+// from the pages' present scales alone, without a look at the values: a scale only ever
+// rises, to the largest among the rows that come in.
 // ---------------------------------------------------------------------------
 constexpr int kMoveThreads = 256;
+constexpr int kMoveRows = kMoveThreads / kRowVec8;  // 7 rows at a time
 constexpr int kMaxTreePages = (DDT_MAX_Q_LEN + 2 * (kPage - 1)) / kPage;  // 3
 static_assert(DDT_MAX_Q_LEN <= kMoveThreads, "one thread per path entry");
 
@@ -477,9 +544,6 @@ __global__ void __launch_bounds__(kMoveThreads) kv_compact_q8_kernel(
       const int page = c.block_table[static_cast<int64_t>(b) * c.max_blocks + blk0 + t];
       bad = page < 0 || page >= c.num_pages;
       s_page[t] = page;
-      const float sc = bad ? 0.f : c.scales[page];
-      s_old[t] = scale_ok(sc) ? sc : 0.f;
-      s_new[t] = __float_as_int(s_old[t]);
     }
     if (t < q_len) s_keep[t] = keep;
     bad |= t < alen && (keep < 0 || keep >= q_len);
@@ -492,17 +556,31 @@ __global__ void __launch_bounds__(kMoveThreads) kv_compact_q8_kernel(
     }
     return;
   }
+  // A thread has one vector of every kMoveRows-th row.
+  const int v = t % kRowVec8;
+  const int64_t step = row_step(c, v);
+  uint8_t* at[kMaxTreePages];
+#pragma unroll
+  for (int g = 0; g < kMaxTreePages; ++g)
+    at[g] = page_vec(c, g <= (o0 + q_len - 1) / kPage ? s_page[g] : 0, v);
+  auto row = [&](int o) {  // of the tree block's pages
+    uint8_t* p = o < kPage ? at[0] : o < 2 * kPage ? at[1] : at[2];
+    return reinterpret_cast<uint4*>(p + (o % kPage) * step);
+  };
+  const int first = t < kMoveRows * kRowVec8 ? t / kRowVec8 : DDT_MAX_Q_LEN;  // no row
+  // All moving rows into shared memory.
+  for (int i = first; i < alen; i += kMoveRows) {
+    const int from = s_keep[i];
+    if (from != i) copy16_async(&s_rows[i * kRowVec8 + v], row(o0 + from));
+  }
+  if (t < (o0 + q_len - 1) / kPage + 1) {  // with the rows, the pages' scales
+    const float sc = c.scales[s_page[t]];
+    s_old[t] = scale_ok(sc) ? sc : 0.f;
+    s_new[t] = __float_as_int(s_old[t]);
+  }
+  __syncthreads();
   if (t < alen)
     atomicMax(&s_new[(o0 + t) / kPage], __float_as_int(s_old[(o0 + keep) / kPage]));
-  // All moving rows into shared memory.
-  const int total = alen * kRowVec8;
-  for (int idx = t; idx < total; idx += kMoveThreads) {
-    const int i = idx / kRowVec8, v = idx - i * kRowVec8;
-    const int from = s_keep[i];
-    if (from == i) continue;
-    const int o = o0 + from;
-    copy16_async(&s_rows[idx], row_vec(c, s_page[o / kPage], o % kPage, v));
-  }
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
   // Pages whose scale rises: every row but those about to be written.
@@ -511,25 +589,23 @@ __global__ void __launch_bounds__(kMoveThreads) kv_compact_q8_kernel(
     const float now = __int_as_float(s_new[g]);
     if (now == s_old[g]) continue;
     const float ratio = s_old[g] / now;
-    for (int idx = t; idx < kPage * kRowVec8; idx += kMoveThreads) {
-      const int r = idx / kRowVec8, v = idx - r * kRowVec8;
+    for (int r = first; r < kPage; r += kMoveRows) {
       const int i = g * kPage + r - o0;
       if (i >= 0 && i < alen && s_keep[i] != i) continue;
-      uint4* p = row_vec(c, s_page[g], r, v);
+      uint4* p = row(g * kPage + r);
       *p = rescale16(*p, ratio);
     }
-    if (t == 0) c.scales[s_page[g]] = now;
   }
-  for (int idx = t; idx < total; idx += kMoveThreads) {
-    const int i = idx / kRowVec8, v = idx - i * kRowVec8;
+  for (int i = first; i < alen; i += kMoveRows) {
     const int from = s_keep[i];
     if (from == i) continue;
-    const int o = o0 + i;
-    const float was = s_old[(o0 + from) / kPage], now = __int_as_float(s_new[o / kPage]);
-    uint4 x = s_rows[idx];
+    const float was = s_old[(o0 + from) / kPage], now = __int_as_float(s_new[(o0 + i) / kPage]);
+    uint4 x = s_rows[i * kRowVec8 + v];
     if (was != now) x = rescale16(x, was / now);
-    *row_vec(c, s_page[o / kPage], o % kPage, v) = x;
+    *row(o0 + i) = x;
   }
+  if (t <= last_blk && __int_as_float(s_new[t]) != s_old[t])
+    c.scales[s_page[t]] = __int_as_float(s_new[t]);
   if (t == 0) {
     if (status) status[b] = DDT_REQ_OK;
     if (new_prefix_lens) new_prefix_lens[b] = P + alen;
@@ -541,24 +617,52 @@ __global__ void __launch_bounds__(kMoveThreads) kv_compact_q8_kernel(
 // ---------------------------------------------------------------------------
 // Launchers
 // ---------------------------------------------------------------------------
+namespace {
+// A launch of `ctas` CTAs in clusters of `cluster`.
+template <typename... Params, typename... Args>
+cudaError_t launch_cluster(void (*kernel)(Params...), unsigned ctas, int cluster, int threads,
+                           cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+}  // namespace
+
 cudaError_t launch_kv_pages(const int32_t* prefix_lens, const int32_t* row_start, int B, int q_len,
                             int64_t n_rows, int num_pages, int max_blocks, int32_t* block_table,
                             int32_t* n_blocks, int32_t* free_pages, int32_t* n_free,
                             int64_t* slots, int32_t* status, cudaStream_t stream) {
-  // Up to four rounds of the planning CTA write their slots there; more rows get a
-  // launch of their own over all SMs.
+  // Few rows: the planning CTAs write their slots; more get a launch of their own over
+  // all SMs.  Few requests: one CTA plans.
   const bool fused = n_rows <= 4 * kPlanThreads;
-  kv_pages_kernel<<<1, kPlanThreads, 0, stream>>>(prefix_lens, row_start, B, q_len,
-                                                  fused ? n_rows : 0, num_pages, max_blocks,
-                                                  block_table, n_blocks, free_pages, n_free, slots,
-                                                  status);
-  if (slots && !fused) {
-    const int64_t ctas = (n_rows + kSlotThreads - 1) / kSlotThreads;
-    const int64_t most = 8ll * device_sm_count();
-    kv_slots_kernel<<<static_cast<unsigned>(ctas < most ? ctas : most), kSlotThreads, 0, stream>>>(
-        prefix_lens, row_start, B, q_len, n_rows, num_pages, max_blocks, block_table, n_blocks,
-        n_free, slots);
+  const int64_t slot_rows = fused ? n_rows : 0;
+  cudaError_t e;
+  if (B <= 256) {
+    kv_pages_kernel<1><<<1, kPlanThreads, 0, stream>>>(
+        prefix_lens, row_start, B, q_len, slot_rows, num_pages, max_blocks, block_table, n_blocks,
+        free_pages, n_free, slots, status);
+    e = cudaGetLastError();
+  } else {
+    e = launch_cluster(kv_pages_kernel<kPlanCtas>, kPlanCtas, kPlanCtas, kPlanThreads, stream,
+                       prefix_lens, row_start, B, q_len, slot_rows, num_pages, max_blocks,
+                       block_table, n_blocks, free_pages, n_free, slots, status);
   }
+  if (e != cudaSuccess || !slots || fused) return e;
+  const int64_t ctas = (n_rows + kSlotRows - 1) / kSlotRows;
+  const int64_t most = 8ll * device_sm_count();
+  kv_slots_kernel<<<static_cast<unsigned>(ctas < most ? ctas : most), kSlotThreads, 0, stream>>>(
+      prefix_lens, row_start, B, q_len, n_rows, num_pages, max_blocks, block_table, n_blocks,
+      n_free, slots);
   return cudaGetLastError();
 }
 
@@ -571,12 +675,17 @@ cudaError_t launch_kv_write_q8(const ddt_q8_cache& c, const int32_t* prefix_lens
   const int64_t pages = (static_cast<int64_t>(max_rows) + 2 * kPage - 2) / kPage;
   const int64_t per = pages > 0 ? pages : 1;
   if (per * B > INT_MAX) return cudaErrorInvalidValue;
-  // The statuses start at OK; a page's CTA can only raise its request's.
-  if (status) {
+  const unsigned ctas = static_cast<unsigned>(per * B);
+  if (per > 1 && per <= kMaxWriteCluster)
+    return launch_cluster(kv_write_q8_kernel<true>, ctas, static_cast<int>(per), kWriteThreads,
+                          stream, c, prefix_lens, row_start, q_len, max_rows, n_rows, rows_ckv,
+                          rows_krope, status, static_cast<int>(per));
+  // The statuses of long prompts start at OK; a page's CTA can only raise its request's.
+  if (status && per > 1) {
     const cudaError_t e = cudaMemsetAsync(status, 0, static_cast<size_t>(B) * sizeof(int32_t), stream);
     if (e != cudaSuccess) return e;
   }
-  kv_write_q8_kernel<<<static_cast<unsigned>(per * B), kWriteThreads, 0, stream>>>(
+  kv_write_q8_kernel<false><<<ctas, kWriteThreads, 0, stream>>>(
       c, prefix_lens, row_start, q_len, max_rows, n_rows, rows_ckv, rows_krope, status,
       static_cast<int>(per));
   return cudaGetLastError();

@@ -58,6 +58,7 @@ namespace ddt {
 static __device__ unsigned int ddt_fault_word = 0;  // this kernel's part, see ddt_fault_flags
 }  // namespace ddt
 
+#include "q8_common.cuh"
 #include "sm100_ptx.cuh"
 #include "verify_shared.cuh"
 
@@ -516,12 +517,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(vq::kThreads, 1)
         for (int r = 0; r < 4; ++r) {
           uint32_t m = 0;
 #pragma unroll
-          for (int j = 0; j < 9; ++j) m = __vmaxu2(m, x[r][j] & 0x7fff7fffu);
-          const uint32_t top = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
-          // 2^e with the row's largest magnitude in (224, 448] * 2^e, from its bf16 bits
-          int e = static_cast<int>(top >> 7) - 127 - 8 + ((top & 0x7fu) > 0x60u);
+          for (int j = 0; j < 9; ++j) m = max_abs_bf16x2(m, x[r][j]);
+          const uint32_t top = __reduce_max_sync(0xffffffffu, max_of_halves(m));
+          int e = e4m3_exponent(top);
           e = top == 0 ? 0 : e < -100 ? -100 : e;
-          const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+          const float inv = pow2f(-e);
           const int row = 16 * u + r0 + r;
           uint32_t hi[4], lo[4];
           uint16_t f[4];
@@ -547,9 +547,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(vq::kThreads, 1)
           *reinterpret_cast<uint16_t*>(at + kQRopeLo - kQRope) = f[1];
           // A row with NaN or an infinity gets NaN as its scale, and so NaN results.
           if (lane == 0)
-            q_scale[slot * 64 + row] = top >= 0x7f80u
-                                           ? __uint_as_float(0x7fc00000u)
-                                           : __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+            q_scale[slot * 64 + row] = top >= 0x7f80u ? __uint_as_float(0x7fc00000u) : pow2f(e);
         }
       }
       fence_proxy_async_smem();

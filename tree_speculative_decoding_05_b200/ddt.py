@@ -439,58 +439,61 @@ def decode_step(args: DecodeArgs, stream=None) -> None:
 # The paged 8-bit latent cache
 # ---------------------------------------------------------------------------
 
-class _OnDevice:
-    """Launches go to the device of the call's tensors, on its current stream (or the
-    given one), whatever device is current; torch's current device is left as it was."""
-
-    __slots__ = ("guard", "stream")
-
-    def __init__(self, device: torch.device, stream):
-        self.guard = (None if device.index == torch.cuda.current_device()
-                      else torch.cuda.device(device))
-        self.stream = (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return self.stream
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+_raw_stream = torch._C._cuda_getCurrentRawStream  # (device index) -> cudaStream_t
 
 
-def _need(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape, device, contiguous=True):
+def _launch(fn, what: str, dev: int, stream, *args) -> None:
+    """fn(*args, stream) on device `dev`, whatever device is current (and stays so), on
+    its current stream or the given one."""
+    s = _raw_stream(dev) if stream is None else stream.cuda_stream
+    if dev == torch.cuda.current_device():
+        rc = fn(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, s)
+    if rc != DDT_OK:
+        _check(rc, what)
+
+
+def _arg(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape: tuple, dev: int,
+         contiguous: bool = True) -> int:
     """The data pointer of an argument of the paged calls (0 for None), once its type,
-    device, shape (None: any size) and layout are what the call takes."""
+    device, shape and layout are what the call takes."""
     if t is None:
         return 0
-    if t.device != device or t.dtype is not dtype:
-        raise DdtError(f"{name} must be {dtype} on {device}, got {t.dtype} on {t.device}")
-    if t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
-        want = "x".join("any" if w is None else str(w) for w in shape)
-        raise DdtError(f"{name} must have shape {want}, got {tuple(t.shape)}")
-    if contiguous and not t.is_contiguous():
-        raise DdtError(f"{name} must be contiguous")
-    return t.data_ptr()
+    if (t.dtype is dtype and t.get_device() == dev and t.shape == shape
+            and (not contiguous or t.is_contiguous())):
+        return t.data_ptr()
+    if t.dtype is not dtype or t.get_device() != dev:
+        raise DdtError(f"{name} must be {dtype} on cuda:{dev}, got {t.dtype} on {t.device}")
+    if t.shape != shape:
+        raise DdtError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    raise DdtError(f"{name} must be contiguous")
 
 
-def _q8_cache(c_kv, k_rope, scales, block_table, B) -> Q8Cache:
-    if not c_kv.is_cuda:
-        raise DdtError("c_kv must be a CUDA tensor")
-    dev, f8 = c_kv.device, torch.float8_e4m3fn
-    pages = c_kv.shape[0]
-    c = Q8Cache()
-    c.c_kv = _need(c_kv, "c_kv", f8, (None, PAGE_ROWS, D_LATENT), dev, contiguous=False)
-    c.k_rope = _need(k_rope, "k_rope", f8, (pages, PAGE_ROWS, D_ROPE), dev, contiguous=False)
-    if c_kv.stride(2) != 1 or k_rope.stride(2) != 1:
+def _dims(t: torch.Tensor, n: int, name: str):
+    if t.dim() != n:
+        raise DdtError(f"{name} must have {n} dimensions, got shape {tuple(t.shape)}")
+    return t.shape
+
+
+def _device_of(t: torch.Tensor, name: str) -> int:
+    if not t.is_cuda:
+        raise DdtError(f"{name} must be a CUDA tensor")
+    return t.get_device()
+
+
+def _q8_cache(c_kv, k_rope, scales, block_table, B: int, dev: int) -> Q8Cache:
+    f8, pages = torch.float8_e4m3fn, _dims(c_kv, 3, "c_kv")[0]
+    width = _dims(block_table, 2, "block_table")[1]
+    ckv = _arg(c_kv, "c_kv", f8, (pages, PAGE_ROWS, D_LATENT), dev, False)
+    kr = _arg(k_rope, "k_rope", f8, (pages, PAGE_ROWS, D_ROPE), dev, False)
+    (cp, cr, ce), (kp, kr_, ke) = c_kv.stride(), k_rope.stride()
+    if ce != 1 or ke != 1:
         raise DdtError("cache rows must be contiguous in their last dimension")
-    c.scales = _need(scales, "scales", torch.float32, (pages,), dev)
-    c.block_table = _need(block_table, "block_table", torch.int32, (B, None), dev)
-    c.ckv_page_stride, c.ckv_row_stride = c_kv.stride(0), c_kv.stride(1)
-    c.kr_page_stride, c.kr_row_stride = k_rope.stride(0), k_rope.stride(1)
-    c.num_pages, c.max_blocks = pages, block_table.shape[1]
-    return c
+    return Q8Cache(ckv, kr, _arg(scales, "scales", torch.float32, (pages,), dev),
+                   _arg(block_table, "block_table", torch.int32, (B, width), dev),
+                   cp, cr, kp, kr_, pages, width)
 
 
 def kv_pages(prefix_lens: torch.Tensor, block_table: torch.Tensor, n_blocks: torch.Tensor,
@@ -504,14 +507,11 @@ def kv_pages(prefix_lens: torch.Tensor, block_table: torch.Tensor, n_blocks: tor
     q_len more rows, or row_start[b+1] - row_start[b] (int32 [B+1]; n_rows is then
     the number of rows of all requests, unless slots tells it).  Returns (slots int64
     [n_rows], status int32 [B])."""
-    if not prefix_lens.is_cuda:
-        raise DdtError("prefix_lens must be a CUDA tensor")
+    dev, (B,) = _device_of(prefix_lens, "prefix_lens"), _dims(prefix_lens, 1, "prefix_lens")
     if (q_len is None) == (row_start is None):
         raise DdtError("give either q_len or row_start")
-    dev, B = prefix_lens.device, prefix_lens.shape[0]
-    i32 = torch.int32
     if q_len is not None:
-        if q_len < 0 or q_len >= 1 << 31:
+        if not 0 <= q_len < 1 << 31:
             raise DdtError(f"q_len must be a row count, got {q_len}")
         if n_rows is not None and n_rows != B * q_len:
             raise DdtError(f"n_rows must be B * q_len = {B * q_len}, got {n_rows}")
@@ -520,19 +520,21 @@ def kv_pages(prefix_lens: torch.Tensor, block_table: torch.Tensor, n_blocks: tor
         if slots is None:
             raise DdtError("row_start needs n_rows or slots")
         n_rows = slots.shape[0]
-    p = (_need(prefix_lens, "prefix_lens", i32, (B,), dev),
-         _need(row_start, "row_start", i32, (B + 1,), dev))
-    state = (_need(block_table, "block_table", i32, (B, None), dev),
-             _need(n_blocks, "n_blocks", i32, (B,), dev),
-             _need(free_pages, "free_pages", i32, (None,), dev),
-             _need(n_free, "n_free", i32, (1,), dev))
-    slots = slots if slots is not None else torch.empty((n_rows,), dtype=torch.int64, device=dev)
-    status = status if status is not None else torch.empty((B,), dtype=i32, device=dev)
-    out = (_need(slots, "slots", torch.int64, (n_rows,), dev),
-           _need(status, "status", i32, (B,), dev))
-    with _OnDevice(dev, stream) as s:
-        _check(load().ddt_kv_pages(*p, B, q_len or 0, n_rows, free_pages.shape[0],
-                                   block_table.shape[1], *state, *out, s), "ddt_kv_pages")
+    i32 = torch.int32
+    width, pages = _dims(block_table, 2, "block_table")[1], _dims(free_pages, 1, "free_pages")[0]
+    if slots is None:
+        slots = torch.empty((n_rows,), dtype=torch.int64, device=prefix_lens.device)
+    if status is None:
+        status = torch.empty_like(prefix_lens)
+    _launch(load().ddt_kv_pages, "ddt_kv_pages", dev, stream,
+            _arg(prefix_lens, "prefix_lens", i32, (B,), dev),
+            _arg(row_start, "row_start", i32, (B + 1,), dev), B, q_len or 0, n_rows, pages, width,
+            _arg(block_table, "block_table", i32, (B, width), dev),
+            _arg(n_blocks, "n_blocks", i32, (B,), dev),
+            _arg(free_pages, "free_pages", i32, (pages,), dev),
+            _arg(n_free, "n_free", i32, (1,), dev),
+            _arg(slots, "slots", torch.int64, (n_rows,), dev),
+            _arg(status, "status", i32, (B,), dev))
     return slots, status
 
 
@@ -546,45 +548,43 @@ def kv_write_q8(c_kv: torch.Tensor, k_rope: torch.Tensor, scales: torch.Tensor,
     float32 [pages], block_table int32 [B, max_blocks].  rows_ckv [B, q_len, 512] and
     rows_krope [B, q_len, 64]; or, with row_start int32 [B+1] and max_rows (no request
     has more), [n_rows, 512] and [n_rows, 64].  Returns status int32 [B]."""
-    B = prefix_lens.shape[0]
-    c = _q8_cache(c_kv, k_rope, scales, block_table, B)
-    dev, i32, bf16 = c_kv.device, torch.int32, torch.bfloat16
+    dev, (B,) = _device_of(c_kv, "c_kv"), _dims(prefix_lens, 1, "prefix_lens")
+    i32, bf16 = torch.int32, torch.bfloat16
     if row_start is None:
         if max_rows is not None:
             raise DdtError("max_rows goes with row_start")
-        q = rows_ckv.shape[1]
+        q = _dims(rows_ckv, 3, "rows_ckv")[1]
         n, max_rows = B * q, q
         lat, rope = (B, q, D_LATENT), (B, q, D_ROPE)
     else:
         if max_rows is None:
             raise DdtError("row_start needs max_rows")
-        n, q = rows_ckv.shape[0], 0
+        n, q = _dims(rows_ckv, 2, "rows_ckv")[0], 0
         lat, rope = (n, D_LATENT), (n, D_ROPE)
-    status = status if status is not None else torch.empty((B,), dtype=i32, device=dev)
-    args = (_need(prefix_lens, "prefix_lens", i32, (B,), dev),
-            _need(row_start, "row_start", i32, (B + 1,), dev), B, q, int(max_rows), n,
-            _need(rows_ckv, "rows_ckv", bf16, lat, dev),
-            _need(rows_krope, "rows_krope", bf16, rope, dev),
-            _need(status, "status", i32, (B,), dev))
-    with _OnDevice(dev, stream) as s:
-        _check(load().ddt_kv_write_q8(ctypes.byref(c), *args, s), "ddt_kv_write_q8")
+    if status is None:
+        status = torch.empty_like(prefix_lens)
+    _launch(load().ddt_kv_write_q8, "ddt_kv_write_q8", dev, stream,
+            _q8_cache(c_kv, k_rope, scales, block_table, B, dev),
+            _arg(prefix_lens, "prefix_lens", i32, (B,), dev),
+            _arg(row_start, "row_start", i32, (B + 1,), dev), B, q, max_rows, n,
+            _arg(rows_ckv, "rows_ckv", bf16, lat, dev),
+            _arg(rows_krope, "rows_krope", bf16, rope, dev),
+            _arg(status, "status", i32, (B,), dev))
     return status
 
 
 def _attn_q8_args(q_lat, q_rope, c_kv, k_rope, scales, block_table, prefix_lens, mask,
                   softmax_scale, max_prefix, num_splits) -> AttnQ8Args:
-    B, Q, H, DL = q_lat.shape
-    dev = c_kv.device
-    a = AttnQ8Args()
-    a.B, a.q_len, a.num_heads, a.d_latent, a.d_rope = B, Q, H, DL, q_rope.shape[3]
-    a.cache = _q8_cache(c_kv, k_rope, scales, block_table, B)
-    a.q_lat = _need(q_lat, "q_lat", torch.bfloat16, (B, Q, H, DL), dev)
-    a.q_rope = _need(q_rope, "q_rope", torch.bfloat16, (B, Q, H, None), dev)
-    a.prefix_lens = _need(prefix_lens, "prefix_lens", torch.int32, (B,), dev)
-    a.mask = _need(mask, "mask", torch.int64, (B, Q, (Q + 63) // 64), dev)
-    a.softmax_scale = float(softmax_scale)
-    a.max_prefix, a.num_splits = int(max_prefix), int(num_splits)
-    return a
+    dev, (B, Q, H, DL) = _device_of(c_kv, "c_kv"), _dims(q_lat, 4, "q_lat")
+    DR = _dims(q_rope, 4, "q_rope")[3]
+    bf16 = torch.bfloat16
+    return AttnQ8Args(B, Q, H, DL, DR, max_prefix,
+                      _q8_cache(c_kv, k_rope, scales, block_table, B, dev),
+                      _arg(prefix_lens, "prefix_lens", torch.int32, (B,), dev),
+                      _arg(q_lat, "q_lat", bf16, (B, Q, H, DL), dev),
+                      _arg(q_rope, "q_rope", bf16, (B, Q, H, DR), dev),
+                      _arg(mask, "mask", torch.int64, (B, Q, (Q + 63) // 64), dev),
+                      None, None, None, 0, None, softmax_scale, num_splits)
 
 
 def verify_attn_q8_workspace_size(q_lat, q_rope, c_kv, k_rope, scales, block_table, prefix_lens,
@@ -595,8 +595,8 @@ def verify_attn_q8_workspace_size(q_lat, q_rope, c_kv, k_rope, scales, block_tab
                       softmax_scale, max_prefix, num_splits)
     lib = load()
     with torch.cuda.device(c_kv.device):
-        return (int(lib.ddt_verify_attn_q8_workspace_size(ctypes.byref(a))),
-                int(lib.ddt_verify_attn_q8_num_splits(ctypes.byref(a))))
+        return (int(lib.ddt_verify_attn_q8_workspace_size(a)),
+                int(lib.ddt_verify_attn_q8_num_splits(a)))
 
 
 def verify_attn_q8(q_lat: torch.Tensor, q_rope: torch.Tensor, c_kv: torch.Tensor,
@@ -612,28 +612,27 @@ def verify_attn_q8(q_lat: torch.Tensor, q_rope: torch.Tensor, c_kv: torch.Tensor
     None)."""
     a = _attn_q8_args(q_lat, q_rope, c_kv, k_rope, scales, block_table, prefix_lens, mask,
                       softmax_scale, max_prefix, num_splits)
-    B, Q, H, dev = a.B, a.q_len, a.num_heads, c_kv.device
+    dev, (B, Q, H, _) = c_kv.get_device(), q_lat.shape
     if out is None:
-        out = torch.empty((B, Q, H, D_LATENT), dtype=torch.bfloat16, device=dev)
+        out = torch.empty((B, Q, H, D_LATENT), dtype=torch.bfloat16, device=c_kv.device)
     if lse is None and want_lse:
-        lse = torch.empty((B, Q, H), dtype=torch.float32, device=dev)
-    a.out = _need(out, "out", torch.bfloat16, (B, Q, H, D_LATENT), dev)
-    a.lse = _need(lse, "lse", torch.float32, (B, Q, H), dev)
-    a.status = _need(status, "status", torch.int32, (B,), dev)
+        lse = torch.empty((B, Q, H), dtype=torch.float32, device=c_kv.device)
+    a.out = _arg(out, "out", torch.bfloat16, (B, Q, H, D_LATENT), dev)
+    a.lse = _arg(lse, "lse", torch.float32, (B, Q, H), dev)
+    a.status = _arg(status, "status", torch.int32, (B,), dev)
     lib = load()
-    with _OnDevice(dev, stream) as s:
-        if workspace is None:
-            need = int(lib.ddt_verify_attn_q8_workspace_size(ctypes.byref(a)))
-            if need:
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-                if stream is not None:  # freed when this returns, read until the call is done
-                    workspace.record_stream(stream)
-        if workspace is not None:
-            if workspace.device != dev:
-                raise DdtError(f"workspace must be on {dev}")
-            a.workspace = workspace.data_ptr()
-            a.workspace_bytes = workspace.numel() * workspace.element_size()
-        _check(lib.ddt_verify_attn_q8(ctypes.byref(a), s), "ddt_verify_attn_q8")
+    if workspace is None:
+        need = lib.ddt_verify_attn_q8_workspace_size(a)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=c_kv.device)
+            if stream is not None:  # freed when this returns, read until the call is done
+                workspace.record_stream(stream)
+    if workspace is not None:
+        if workspace.get_device() != dev:
+            raise DdtError(f"workspace must be on cuda:{dev}")
+        a.workspace = workspace.data_ptr()
+        a.workspace_bytes = workspace.numel() * workspace.element_size()
+    _launch(lib.ddt_verify_attn_q8, "ddt_verify_attn_q8", dev, stream, a)
     return out, lse
 
 
@@ -644,17 +643,19 @@ def kv_compact_q8(c_kv: torch.Tensor, k_rope: torch.Tensor, scales: torch.Tensor
     """In-place compaction of the accepted rows in the paged 8-bit cache; pass
     new_prefix_lens=prefix_lens to update the prefix lengths in place.  Returns
     (new_prefix_lens, status)."""
-    B, Q = path.shape
-    c = _q8_cache(c_kv, k_rope, scales, block_table, B)
-    dev, i32 = c_kv.device, torch.int32
-    new = new_prefix_lens if new_prefix_lens is not None else torch.empty((B,), dtype=i32, device=dev)
-    status = status if status is not None else torch.empty((B,), dtype=i32, device=dev)
-    args = (_need(prefix_lens, "prefix_lens", i32, (B,), dev), _need(path, "path", i32, (B, Q), dev),
-            _need(accept_len, "accept_len", i32, (B,), dev), B, Q,
-            _need(new, "new_prefix_lens", i32, (B,), dev), _need(status, "status", i32, (B,), dev))
-    with _OnDevice(dev, stream) as s:
-        _check(load().ddt_kv_compact_q8(ctypes.byref(c), *args, s), "ddt_kv_compact_q8")
-    return new, status
+    dev, (B, Q), i32 = _device_of(c_kv, "c_kv"), _dims(path, 2, "path"), torch.int32
+    if new_prefix_lens is None:
+        new_prefix_lens = torch.empty_like(prefix_lens)
+    if status is None:
+        status = torch.empty_like(prefix_lens)
+    _launch(load().ddt_kv_compact_q8, "ddt_kv_compact_q8", dev, stream,
+            _q8_cache(c_kv, k_rope, scales, block_table, B, dev),
+            _arg(prefix_lens, "prefix_lens", i32, (B,), dev),
+            _arg(path, "path", i32, (B, Q), dev),
+            _arg(accept_len, "accept_len", i32, (B,), dev), B, Q,
+            _arg(new_prefix_lens, "new_prefix_lens", i32, (B,), dev),
+            _arg(status, "status", i32, (B,), dev))
+    return new_prefix_lens, status
 
 
 def selftest_bounded_wait(timeout_us: int = 2000, stream=None) -> torch.Tensor:
