@@ -584,8 +584,8 @@ DDT_API ddt_status ddt_kv_write_q8(const ddt_q8_cache* cache, const int32_t* pre
  * row's largest value); softmax weights likewise (relative error at most 2^-8,
  * as a bf16 weight's); scores, sums and the output accumulate in fp32.
  *
- * out is bf16 [B, q_len, 64, 512] (the weights' 8 bits would not fill an fp32
- * output), lse fp32 [B, q_len, 64] or NULL, with the meaning of ddt_verify_attn;
+ * out is bf16 [B, q_len, 64, 512], 32-byte aligned (the weights' 8 bits would not
+ * fill an fp32 output), lse fp32 [B, q_len, 64] or NULL, with the meaning of ddt_verify_attn;
  * a row that sees no key gives 0 and -inf.  Cache rows at or past P + q_len are
  * never read.  A NaN byte in a row of the request makes the whole request's
  * outputs NaN at that column, whether a node sees the row or not (0 * NaN);

@@ -472,7 +472,7 @@ ddt_status ddt_verify_attn_q8(const ddt_attn_q8_args* a, ddt_stream_t stream) {
   if (st != DDT_OK || a->B == 0) return st;
   if (!q8_cache_ok(a->cache) || !a->prefix_lens || !a->q_lat || !a->q_rope || !a->mask || !a->out)
     return DDT_ERR_INVALID_ARG;
-  if (!aligned16(a->q_lat) || !aligned16(a->q_rope) || !aligned16(a->out))
+  if (!aligned16(a->q_lat) || !aligned16(a->q_rope) || (reinterpret_cast<uintptr_t>(a->out) & 31u))
     return DDT_ERR_INVALID_ARG;
   if (plain.capacity < a->q_len) return DDT_ERR_INVALID_ARG;
   if (!softmax_scale_ok(a->softmax_scale)) return DDT_ERR_INVALID_ARG;

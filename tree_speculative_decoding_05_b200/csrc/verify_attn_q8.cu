@@ -34,20 +34,17 @@
 //     rows before the page's first with zeros and never reads those behind the sequence,
 //     which may hold anything.
 //   * TMEM per CTA: four S buffers (4 x 64 columns) + O (256 columns).
-//   * warps 0-7 softmax and epilogue, two threads for each half row (32 keys each): with
-//     one, its 64 exponentials and splits outlast the MMAs of a tile (64 requests x 33
-//     nodes x 4096 rows: 1225 us, against 1098 us with two, back to back); 8 and 12 fill
-//     the K rings of even and odd tiles, 10 the V ring; 9, 14 issue S of even and odd
-//     tiles and 11 issues P V (on three sub-partitions); 13 checks a request's page
-//     numbers for its status; 15-18 split the next item's queries while this one's last
-//     tiles are at work.
+//   * warps 0-7 softmax, two threads for each half row (32 keys each); 8 and 12 fill the
+//     K rings of even and odd tiles, 10 the V ring; 9, 14 issue S of even and odd tiles
+//     and 11 issues P V (on three sub-partitions); 13 checks a request's page numbers for
+//     its status; 15-18 split the next item's queries while this one's last tiles are at
+//     work, and then write this item's output while the softmax warps go on to the next.
 //   * S runs up to three tiles ahead of the softmax; O is rescaled only when the running
 //     maximum outgrows its reference by 2^2.75.
 //   * long caches: splits write normalised partials, merged by the bf16 call's merge.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
-#include <climits>
 #include <cmath>
 #include <cstdint>
 
@@ -84,6 +81,7 @@ constexpr int kKSlotBytes = 2 * kBox + kBox / 2;
 constexpr int kVSlots = 4;                     // 64 keys x 128 columns each
 constexpr int kPBufBytes = 2 * kBox;           // 64 rows x 128 keys: hi, lo
 constexpr int kPBufs = 2;
+constexpr int kLSlots = 4;                     // row sums of up to 4 items, see below
 constexpr int kQSlots = 8;                     // row scales of up to 8 items, see below
 constexpr int kMaxSortedB = 512;
 constexpr int kOffQ = 0;
@@ -92,10 +90,11 @@ constexpr int kOffVRing = kOffKRing + 2 * kKSlots * kKSlotBytes;
 constexpr int kOffP = kOffVRing + kVSlots * kBox;
 constexpr int kOffRedMax = kOffP + kPBufs * kPBufBytes;
 constexpr int kOffRedL = kOffRedMax + 2 * 256 * 4;  // red_max: float[2][4][64]
-constexpr int kOffQScale = kOffRedL + 256 * 4;  // float[kQSlots][64]
-constexpr int kOffLen = kOffQScale + kQSlots * 64 * 4;
-constexpr int kOffOrder = kOffLen + kMaxSortedB * 4;
-constexpr int kOffBar = kOffOrder + kMaxSortedB * 4;
+constexpr int kRedL = 5 * 64;                       // red_l: four parts of each row sum, its maximum
+constexpr int kOffQScale = kOffRedL + kLSlots * kRedL * 4;  // bf16[kQSlots][64]
+constexpr int kOffOrder = kOffQScale + kQSlots * 64 * 2;  // uint16[kMaxSortedB]
+constexpr int kOffBar = kOffOrder + kMaxSortedB * 2;
+constexpr int kOffLen = kOffP;  // int[kMaxSortedB], before the first tile
 constexpr int kBarKFull = 0;  // ring g at g * kKSlots
 constexpr int kBarKEmpty = kBarKFull + 2 * kKSlots;
 constexpr int kBarVFull = kBarKEmpty + 2 * kKSlots;
@@ -109,14 +108,14 @@ constexpr int kBarP = kBarSFree + 4;
 constexpr int kBarO = kBarP + kPBufs;        // four: P V of tile G done (G % 4)
 constexpr int kBarQKDone = kBarO + 4;
 constexpr int kBarPVDone = kBarQKDone + 2;
-constexpr int kBarOFree = kBarPVDone + 1;
-constexpr int kNumBars = kBarOFree + 1;
+constexpr int kBarOFree = kBarPVDone + 1;      // both CTAs have read O
+constexpr int kBarL = kBarOFree + 1;           // this CTA's row sums of item i (i % kLSlots)
+constexpr int kNumBars = kBarL + kLSlots;
 constexpr int kOffTmemPtr = kOffBar + kNumBars * 8;
 constexpr int kOffAbort = kOffTmemPtr + 4;
 constexpr int kSmemUsed = kOffAbort + 4;
 constexpr int kSmemBytes = kSmemUsed + 1024;  // slack for 1024-byte alignment
 static_assert(kSmemBytes <= 232448, "shared memory budget");
-static_assert(kPBufs * kPBufBytes >= 64 * 256 * 2, "P buffers hold half an output tile");
 
 constexpr int kTmemCols = 512, kTmemS = 0, kTmemO = 256;
 constexpr uint32_t kIdescQK = idesc_e4m3_f32(128, kTK, false);
@@ -134,8 +133,10 @@ struct Params {
   const uint16_t* q_lat;
   const uint16_t* q_rope;
   const uint64_t* mask;
+  uint16_t* out;
   float* lse;
-  float* part_lse;
+  float* part_o;    // [num_splits][B * Q * 64][512]
+  float* part_lse;  // [num_splits][B * Q * 64]
   int32_t* status;
   int B, Q, num_pages, max_blocks, num_splits, n_pairs, write_partials;
   float scale_log2;  // softmax_scale * log2(e)
@@ -146,7 +147,7 @@ struct Item {
   bool bad_prefix, valid;
 };
 
-__device__ __forceinline__ Item decode_item(const Params& p, int w, const int* order) {
+__device__ __forceinline__ Item decode_item(const Params& p, int w, const uint16_t* order) {
   Item it;
   const int per_req = p.n_pairs * p.num_splits;
   const int slot = w / per_req;
@@ -210,6 +211,51 @@ __device__ __forceinline__ uint32_t pack16(uint16_t lo, uint16_t hi) {
   return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
 }
 
+// One query row, by a warp: a lane has latent values 16 lane .. + 15 (x[0 .. 7]) and rope
+// values 2 lane, 2 lane + 1 (x[8]).
+__device__ __forceinline__ void split_row(const uint32_t (&x)[9], uint8_t* q, int row, int lane,
+                                          uint16_t* scale) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < 9; ++j) m = max_abs_bf16x2(m, x[j]);
+  const uint32_t top = __reduce_max_sync(0xffffffffu, max_of_halves(m));
+  int e = e4m3_exponent(top);
+  e = top == 0 ? 0 : e < -100 ? -100 : e;
+  const float inv = pow2f(-e);
+  uint32_t hi[5], lo[5];
+#pragma unroll
+  for (int j = 0; j < 5; ++j) {
+    uint16_t f[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int v = 0; v < (j < 4 ? 2 : 1); ++v) {
+      const uint32_t h = x[2 * j + v];
+      split_e4m3x2(__uint_as_float(h << 16) * inv, __uint_as_float(h & 0xffff0000u) * inv, f[v],
+                   f[2 + v]);
+    }
+    hi[j] = pack16(f[0], f[1]);
+    lo[j] = pack16(f[2], f[3]);
+  }
+  uint8_t* at = q + (lane >> 3) * kBox + row * 128 + (((lane & 7) ^ (row & 7)) << 4);
+  *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+  *reinterpret_cast<uint4*>(at + kQLo) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+  at = q + kQRope + row * 64 + (((lane >> 3) ^ ((row >> 1) & 3)) << 4) + 2 * (lane & 7);
+  *reinterpret_cast<uint16_t*>(at) = static_cast<uint16_t>(hi[4]);
+  *reinterpret_cast<uint16_t*>(at + kQRopeLo - kQRope) = static_cast<uint16_t>(lo[4]);
+  // A row with NaN or an infinity gets NaN as its scale, and so NaN results.
+  if (lane == 0) scale[row] = top >= 0x7f80u ? 0x7fc0 : static_cast<uint16_t>((e + 127) << 7);
+}
+
+// 32 bytes, aligned to a sector.
+__device__ __forceinline__ void store_sector(void* at, const uint32_t (&y)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(y[0]), "r"(y[1]),
+               "r"(y[2]), "r"(y[3]), "r"(y[4]), "r"(y[5]), "r"(y[6]), "r"(y[7])
+               : "memory");
+}
+
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+
 }  // namespace vq
 
 // Persistent kernel: each CTA pair loops over work items (see work_index); rings,
@@ -217,8 +263,7 @@ __device__ __forceinline__ uint32_t pack16(uint16_t lo, uint16_t hi) {
 // of all items that a CTA has seen.
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(vq::kThreads, 1)
     verify_attn_q8_kernel(const __grid_constant__ CUtensorMap tm_lat,
-                          const __grid_constant__ CUtensorMap tm_rope,
-                          const __grid_constant__ CUtensorMap tm_out, const vq::Params p) {
+                          const __grid_constant__ CUtensorMap tm_rope, const vq::Params p) {
   using namespace vq;
   const uint32_t rank = cluster_ctarank();
   const int cluster = static_cast<int>(blockIdx.x >> 1);
@@ -236,7 +281,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(vq::kThreads, 1)
   const uint32_t sP = base_addr + kOffP;
   float* red_max = reinterpret_cast<float*>(base + kOffRedMax);
   float* red_l = reinterpret_cast<float*>(base + kOffRedL);
-  float* q_scale = reinterpret_cast<float*>(base + kOffQScale);
+  uint16_t* q_scale = reinterpret_cast<uint16_t*>(base + kOffQScale);  // as bf16, a power of two
   const uint32_t bars = base_addr + kOffBar;
   auto bar = [&](int i) -> uint32_t { return bars + 8u * static_cast<uint32_t>(i); };
   uint32_t* tmem_ptr_smem = reinterpret_cast<uint32_t*>(base + kOffTmemPtr);
@@ -265,7 +310,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(vq::kThreads, 1)
     for (int s = 0; s < kPBufs; ++s) mbar_init(bar(kBarP + s), 2);
     for (int g = 0; g < 2; ++g) mbar_init(bar(kBarQKDone + g), 1);
     mbar_init(bar(kBarPVDone), 1);
-    mbar_init(bar(kBarOFree), 2);
+    mbar_init(bar(kBarOFree), 2 * kQWarps);  // every writing warp of the pair
+    for (int s = 0; s < kLSlots; ++s) mbar_init(bar(kBarL + s), kSoftmaxThreads);
     *abort_flag = 0;
     fence_mbar_init_cluster();
   }
@@ -273,33 +319,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(vq::kThreads, 1)
     tmem_alloc<2>(smem_u32(tmem_ptr_smem), kTmemCols);
     tmem_relinquish<2>();
   }
-  // Requests by decreasing length (ties by index), found by every CTA for itself.
+  // Requests by decreasing length (ties by index), found by every CTA for itself; equal
+  // lengths need no look at each other.
   int* len_smem = reinterpret_cast<int*>(base + kOffLen);
-  int* order_smem = reinterpret_cast<int*>(base + kOffOrder);
+  uint16_t* order_smem = reinterpret_cast<uint16_t*>(base + kOffOrder);
   const bool sorted = p.B <= kMaxSortedB;
   if (sorted) {
+    int differs = 0;
     for (int b = threadIdx.x; b < p.B; b += kThreads) {
       const int P = p.prefix_lens[b];
       len_smem[b] = P < 0 || static_cast<int64_t>(P) + Q > static_cast<int64_t>(p.max_blocks) * kPage
                         ? 0 : P + Q;
+      differs |= P != p.prefix_lens[0];
     }
-    __syncthreads();
-    for (int bi = warp; bi < p.B; bi += kThreads / 32) {
+    differs = __syncthreads_or(differs);
+    for (int bi = threadIdx.x; bi < p.B; bi += kThreads) {
       const int li = len_smem[bi];
-      int before = 0;
-      for (int bj = lane; bj < p.B; bj += 32) {
-        const int lj = len_smem[bj];
-        before += lj > li || (lj == li && bj < bi);
+      int before = differs ? 0 : bi;
+      if (differs) {
+#pragma unroll 8
+        for (int bj = 0; bj < p.B; ++bj) {
+          const int lj = len_smem[bj];
+          before += lj > li || (lj == li && bj < bi);
+        }
       }
-      before = __reduce_add_sync(0xffffffffu, before);
-      if (lane == 0) order_smem[before] = bi;
+      order_smem[before] = static_cast<uint16_t>(bi);
     }
   }
   tc_fence_before_sync();
   cluster_sync();
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_ptr_smem;
-  const int* order = sorted ? order_smem : nullptr;
+  const uint16_t* order = sorted ? order_smem : nullptr;
 
   struct Ring {
     int stage = 0;
@@ -379,11 +430,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(vq::kThreads, 1)
     __syncwarp();
   } else if (warp == kWarpSIss0 || warp == kWarpSIss1) {
     // -------------------------------------------------------- MMA: S = Q K^T
-    // Issuer g takes tiles G with G % 2 == g; tile G goes to S buffer G % 4.
-    if (leader && lane == 0) {
+    // Issuer g takes tiles G with G % 2 == g; tile G goes to S buffer G % 4.  The whole
+    // warp runs the loop and one lane issues: descriptors then stay in uniform registers
+    // and an MMA goes out every 32 cycles, its own time, where a lone lane's loop manages
+    // one in 68.
+    if (leader) {
+      const bool one = elect_one();
       const int g = ring_g;
       const int full0 = kBarKFull + g * kKSlots, empty0 = kBarKEmpty + g * kKSlots;
       const uint32_t ring = base_addr + kOffKRing + g * kKSlots * kKSlotBytes;
+      const uint64_t q_desc = smem_desc_sw128(sQ, 16, 1024);
+      const uint64_t rope_desc = smem_desc_sw64(sQ + kQRope);
       Ring r;
       int iter = 0;
       int64_t G = 0;
@@ -401,42 +458,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(vq::kThreads, 1)
             tc_fence_after_sync();
           }
           const uint32_t d = tmem + kTmemS + 64u * static_cast<uint32_t>(sbuf);
+#pragma unroll
           for (int half = 0; half < 2; ++half) {
             mbar_wait(bar(full0 + r.stage), r.phase, abort_flag);
             const uint32_t slot = ring + r.stage * kKSlotBytes;
-            for (int u = 0; u < 2; ++u) {
-              const uint32_t a0 = sQ + (2 * half + u) * kBox;
+            const uint64_t k_desc = smem_desc_sw128(slot, 16, 1024);
 #pragma unroll
-              for (int ks = 0; ks < 4; ++ks) {
-                const uint64_t kd = smem_desc_sw128(slot + u * kBox + 32 * ks, 16, 1024);
-                mma_f8_ss<2>(d, smem_desc_sw128(a0 + 32 * ks, 16, 1024), kd, kIdescQK,
-                             (half | u | ks) != 0);
-                mma_f8_ss<2>(d, smem_desc_sw128(a0 + kQLo + 32 * ks, 16, 1024), kd, kIdescQK, 1);
-              }
+            for (int i = 0; i < 8; ++i) {
+              const uint64_t kd = k_desc + (((i >> 2) * kBox + 32 * (i & 3)) >> 4);
+              const uint64_t qd = q_desc + (((2 * half + (i >> 2)) * kBox + 32 * (i & 3)) >> 4);
+              if (one) mma_f8_ss<2>(d, qd, kd, kIdescQK, half + i != 0);
+              if (one) mma_f8_ss<2>(d, qd + (kQLo >> 4), kd, kIdescQK, 1);
             }
             if (half == 0) {
+              const uint64_t r_desc = smem_desc_sw64(slot + kKRopeOff);
 #pragma unroll
               for (int ks = 0; ks < 2; ++ks) {
-                const uint64_t kd = smem_desc_sw64(slot + kKRopeOff + 32 * ks);
-                mma_f8_ss<2>(d, smem_desc_sw64(sQ + kQRope + 32 * ks), kd, kIdescQK, 1);
-                mma_f8_ss<2>(d, smem_desc_sw64(sQ + kQRopeLo + 32 * ks), kd, kIdescQK, 1);
+                if (one) mma_f8_ss<2>(d, rope_desc + 2 * ks, r_desc + 2 * ks, kIdescQK, 1);
+                if (one)
+                  mma_f8_ss<2>(d, rope_desc + ((kQRopeLo - kQRope) >> 4) + 2 * ks, r_desc + 2 * ks,
+                               kIdescQK, 1);
               }
             }
-            mma_commit<2>(bar(empty0 + r.stage), 0x3);
+            if (one) mma_commit<2>(bar(empty0 + r.stage), 0x3);
             r.advance(kKSlots);
           }
-          mma_commit<2>(bar(kBarS + sbuf), 0x3);
+          if (one) mma_commit<2>(bar(kBarS + sbuf), 0x3);
         }
-        mma_commit<2>(bar(kBarQFree), 0x3);  // this issuer no longer reads this item's Q
+        if (one) mma_commit<2>(bar(kBarQFree), 0x3);  // this issuer no longer reads this item's Q
         ++iter;
       }
-      mma_commit<2>(bar(kBarQKDone + g), 0x1);
+      if (one) mma_commit<2>(bar(kBarQKDone + g), 0x1);
+      __syncwarp();
       mbar_wait(bar(kBarQKDone + g), 0, abort_flag);
     }
     __syncwarp();
   } else if (warp == kWarpPVIss) {
     // ---------------------------------------------------------- MMA: O += P V
-    if (leader && lane == 0) {
+    if (leader) {
+      const bool one = elect_one();
       Ring r;
       int iter = 0;
       int64_t G = 0;
@@ -445,7 +505,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(vq::kThreads, 1)
         if (w < 0) continue;
         const Item it = decode_item(p, w, order);
         if (!it.valid) continue;
-        if (iter > 0) {  // both epilogues have read the previous item's O
+        if (iter > 0) {  // both CTAs' output warps have read the previous item's O
           mbar_wait(bar(kBarOFree), static_cast<uint32_t>((iter - 1) & 1), abort_flag);
           tc_fence_after_sync();
         }
@@ -453,49 +513,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(vq::kThreads, 1)
           const int pb = static_cast<int>(G % kPBufs);
           mbar_wait(bar(kBarP + pb), static_cast<uint32_t>((G / kPBufs) & 1), abort_flag);
           tc_fence_after_sync();
-          for (int kb = 0; kb < 2; ++kb) {
-            for (int nh = 0; nh < 2; ++nh) {
-              mbar_wait(bar(kBarVFull + r.stage), r.phase, abort_flag);
-              const uint32_t d = tmem + kTmemO + 128u * static_cast<uint32_t>(nh);
-              const uint32_t a0 = sP + pb * kPBufBytes + kPage * kb;
-              const uint32_t b0 = sVRing + r.stage * kBox;
+          const uint64_t p_desc = smem_desc_sw128(sP + pb * kPBufBytes, 16, 1024);
 #pragma unroll
-              for (int ks = 0; ks < 2; ++ks) {
-                const uint64_t vd = smem_desc_sw128(b0 + 4096 * ks, kBox, 1024);
-                mma_f8_ss<2>(d, smem_desc_sw128(a0 + 32 * ks, 16, 1024), vd, kIdescPV,
-                             !(jj == 0 && kb == 0 && ks == 0));
-                mma_f8_ss<2>(d, smem_desc_sw128(a0 + kBox + 32 * ks, 16, 1024), vd, kIdescPV, 1);
-              }
-              mma_commit<2>(bar(kBarVEmpty + r.stage), 0x3);
-              r.advance(kVSlots);
+          for (int i = 0; i < 4; ++i) {  // page i / 2, column half i % 2
+            mbar_wait(bar(kBarVFull + r.stage), r.phase, abort_flag);
+            const uint32_t d = tmem + kTmemO + 128u * (i & 1);
+            const uint64_t v_desc = smem_desc_sw128(sVRing + r.stage * kBox, kBox, 1024);
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+              const uint64_t pd = p_desc + ((kPage * (i >> 1) + 32 * ks) >> 4);
+              const uint64_t vd = v_desc + ((4096 * ks) >> 4);
+              if (one) mma_f8_ss<2>(d, pd, vd, kIdescPV, jj > 0 || i >= 2 || ks > 0);
+              if (one) mma_f8_ss<2>(d, pd + (kBox >> 4), vd, kIdescPV, 1);
             }
+            if (one) mma_commit<2>(bar(kBarVEmpty + r.stage), 0x3);
+            r.advance(kVSlots);
           }
-          mma_commit<2>(bar(kBarO + static_cast<int>(G & 3)), 0x3);
+          if (one) mma_commit<2>(bar(kBarO + static_cast<int>(G & 3)), 0x3);
         }
         ++iter;
       }
-      mma_commit<2>(bar(kBarPVDone), 0x1);
+      if (one) mma_commit<2>(bar(kBarPVDone), 0x1);
+      __syncwarp();
       mbar_wait(bar(kBarPVDone), 0, abort_flag);
     }
     __syncwarp();
   } else if (warp >= kWarpQ0) {
-    // ------------------------------------------------- queries to e4m3 hi + lo
-    // Warp u splits rows 16 u .. 16 u + 15 of this CTA's node.  A lane holds latent
-    // values 16 lane .. + 15 and rope values 2 lane, 2 lane + 1 of a row; four rows are
-    // loaded at a time, the first four before the wait for the previous item's S.
+    // ----------------------- queries to e4m3 hi + lo, and outputs to memory
     const int u = warp - kWarpQ0;
     const uint32_t q_bar = map_to_rank(bar(kBarQ), 0);
-    int iter = 0;
-    for (int k = 0; k < n_rounds; ++k) {
-      const int w = work_index(k, cluster, n_clusters, n_items);
-      if (w < 0) continue;
-      const Item it = decode_item(p, w, order);
-      if (!it.valid) continue;
+    const uint32_t o_free_leader = map_to_rank(bar(kBarOFree), 0);
+    // Rows 16 u .. 16 u + 15 of this CTA's node of item `it`, the iter-th one.
+    auto split_queries = [&](const Item& it, int iter) {
       const int node = 2 * it.pair + static_cast<int>(rank);
       const int64_t row0 = (static_cast<int64_t>(it.b) * Q + node) * 64 + 16 * u;
       const uint4* lat = reinterpret_cast<const uint4*>(p.q_lat) + row0 * 64 + 2 * lane;
       const uint32_t* rope = reinterpret_cast<const uint32_t*>(p.q_rope) + row0 * 32 + lane;
-      const int slot = iter % kQSlots;
+      uint16_t* scale = q_scale + iter % kQSlots * 64;
+      if (node < Q) {  // 16 rows of 1024 and of 128 bytes, one line a lane
+#pragma unroll
+        for (int i = 0; i < 4; ++i) prefetch_l2(p.q_lat + row0 * 512 + (32 * i + lane) * 64);
+        if (lane < 16) prefetch_l2(p.q_rope + row0 * 64 + lane * 64);
+      }
 #pragma unroll 1
       for (int r0 = 0; r0 < 16; r0 += 4) {
         uint32_t x[4][9];
@@ -514,49 +573,111 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(vq::kThreads, 1)
         if (r0 == 0 && iter > 0)
           mbar_wait(bar(kBarQFree), static_cast<uint32_t>((iter - 1) & 1), abort_flag);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          uint32_t m = 0;
-#pragma unroll
-          for (int j = 0; j < 9; ++j) m = max_abs_bf16x2(m, x[r][j]);
-          const uint32_t top = __reduce_max_sync(0xffffffffu, max_of_halves(m));
-          int e = e4m3_exponent(top);
-          e = top == 0 ? 0 : e < -100 ? -100 : e;
-          const float inv = pow2f(-e);
-          const int row = 16 * u + r0 + r;
-          uint32_t hi[4], lo[4];
-          uint16_t f[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-#pragma unroll
-            for (int v = 0; v < 2; ++v) {
-              const uint32_t h = x[r][2 * j + v];
-              split_e4m3x2(__uint_as_float(h << 16) * inv, __uint_as_float(h & 0xffff0000u) * inv,
-                           f[v], f[2 + v]);
-            }
-            hi[j] = pack16(f[0], f[1]);
-            lo[j] = pack16(f[2], f[3]);
-          }
-          uint8_t* at = base + kOffQ + (lane >> 3) * kBox + row * 128 + (((lane & 7) ^ (row & 7)) << 4);
-          *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(at + kQLo) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          const uint32_t h = x[r][8];
-          split_e4m3x2(__uint_as_float(h << 16) * inv, __uint_as_float(h & 0xffff0000u) * inv, f[0],
-                       f[1]);
-          at = base + kOffQ + kQRope + row * 64 + (((lane >> 3) ^ ((row >> 1) & 3)) << 4) + 2 * (lane & 7);
-          *reinterpret_cast<uint16_t*>(at) = f[0];
-          *reinterpret_cast<uint16_t*>(at + kQRopeLo - kQRope) = f[1];
-          // A row with NaN or an infinity gets NaN as its scale, and so NaN results.
-          if (lane == 0)
-            q_scale[slot * 64 + row] = top >= 0x7f80u ? __uint_as_float(0x7fc00000u) : pow2f(e);
-        }
+        for (int r = 0; r < 4; ++r) split_row(x[r], base + kOffQ, 16 * u + r0 + r, lane, scale);
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive_local(bar(kBarQScale + slot));
+        mbar_arrive_local(bar(kBarQScale + iter % kQSlots));
         mbar_arrive_cluster(q_bar);
       }
-      ++iter;
+    };
+    int k = 0;
+    auto next_item = [&](Item& it) {
+      for (; k < n_rounds; ++k) {
+        const int w = work_index(k, cluster, n_clusters, n_items);
+        if (w < 0) continue;
+        it = decode_item(p, w, order);
+        if (it.valid) {
+          ++k;
+          return true;
+        }
+      }
+      return false;
+    };
+    Item cur, nxt;
+    bool have = next_item(cur);
+    if (have) split_queries(cur, 0);
+    int64_t G = 0;
+    const int t = (warp & 3) * 32 + lane;  // TMEM lane
+    const int m = t & 63, hf = t >> 6;
+    const uint32_t lane_addr = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    for (int iter = 0; have; ++iter) {
+      const bool more = next_item(nxt);
+      if (more) split_queries(nxt, iter + 1);
+      // The row sums of item i lie in slot i % 4: softmax is at most three items ahead
+      // of the output (two P buffers, and P V of item i + 1 waits for item i's output).
+      G += cur.ntile;
+      const float* red = red_l + iter % kLSlots * kRedL;
+      mbar_wait(bar(kBarL + iter % kLSlots), static_cast<uint32_t>((iter / kLSlots) & 1), abort_flag);
+      const float l_row = (red[m] + red[64 + m]) + (red[128 + m] + red[192 + m]);
+      const float m_use = red[256 + m];
+      const bool empty_row = l_row == 0.f;
+      const float inv = empty_row ? 0.f : 1.f / l_row;
+      const float lse_nat = empty_row ? -INFINITY : (m_use - kBase + __log2f(l_row)) * kLn2;
+      const int node = 2 * cur.pair + static_cast<int>(rank);
+      const int64_t row = (static_cast<int64_t>(cur.b) * Q + node) * 64 + m;
+      mbar_wait(bar(kBarO + static_cast<int>((G - 1) & 3)), static_cast<uint32_t>(((G - 1) >> 2) & 1),
+                abort_flag);
+      tc_fence_after_sync();
+      // Lane t has columns 256 nh + 128 hf + 0 .. 127 of its row; 32 at a time, each a
+      // run of whole 32-byte sectors.
+      if (node < Q) {
+        if (!p.write_partials) {
+          uint16_t* out = p.out + row * DDT_D_LATENT + 128 * hf;
+#pragma unroll 2
+          for (int q = 0; q < 8; ++q) {
+            uint32_t o[32];
+            tmem_ld32(tmem + lane_addr + kTmemO + 32u * q, o);
+            tmem_wait_ld();
+            if (q == 7) {
+              tc_fence_before_sync();
+              __syncwarp();
+              if (lane == 0) mbar_arrive_cluster(o_free_leader);
+            }
+            uint16_t* at = out + 256 * (q >> 2) + 32 * (q & 3);
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+              uint32_t y[8];
+#pragma unroll
+              for (int z = 0; z < 8; ++z)
+                y[z] = pack_bf16x2(__uint_as_float(o[16 * v + 2 * z]) * inv,
+                                   __uint_as_float(o[16 * v + 2 * z + 1]) * inv);
+              store_sector(at + 16 * v, y);
+            }
+          }
+          if (hf == 0 && p.lse) p.lse[row] = lse_nat;
+        } else {  // a split's normalised fp32 partial
+          const int64_t prow = cur.split * static_cast<int64_t>(p.B) * Q * 64 + row;
+          float* out = p.part_o + prow * DDT_D_LATENT + 128 * hf;
+#pragma unroll 2
+          for (int q = 0; q < 8; ++q) {
+            uint32_t o[32];
+            tmem_ld32(tmem + lane_addr + kTmemO + 32u * q, o);
+            tmem_wait_ld();
+            if (q == 7) {
+              tc_fence_before_sync();
+              __syncwarp();
+              if (lane == 0) mbar_arrive_cluster(o_free_leader);
+            }
+            float* at = out + 256 * (q >> 2) + 32 * (q & 3);
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              uint32_t y[8];
+#pragma unroll
+              for (int z = 0; z < 8; ++z) y[z] = __float_as_uint(__uint_as_float(o[8 * v + z]) * inv);
+              store_sector(at + 8 * v, y);
+            }
+          }
+          if (hf == 0) p.part_lse[prow] = lse_nat;
+        }
+      } else {  // a node past q_len (odd q_len): nothing to write
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(o_free_leader);
+      }
+      cur = nxt;
+      have = more;
     }
   } else if (warp == kWarpStatus) {
     // A request's status, by the even CTA that has its first pair and split: whether
@@ -591,7 +712,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(vq::kThreads, 1)
     const int W = (Q + 63) >> 6;
     const uint32_t p_full_leader0 = map_to_rank(bar(kBarP), 0);
     const uint32_t s_free_leader0 = map_to_rank(bar(kBarSFree), 0);
-    const uint32_t o_free_leader = map_to_rank(bar(kBarOFree), 0);
     // P V completions, confirmed in tile order on four barriers; the softmax waits at
     // most for tile G - kPBufs while P V has finished at most tile G - 1.
     int64_t o_next = 0;
@@ -612,7 +732,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(vq::kThreads, 1)
       if (w < 0) continue;
       const Item it = decode_item(p, w, order);
       if (!it.valid) continue;
-      const int b = it.b, P = it.P, split = it.split;
+      const int b = it.b, P = it.P;
       const int node = 2 * it.pair + static_cast<int>(rank);
       const bool node_valid = node < Q;
       uint64_t mw0 = 0, mw1 = 0;
@@ -634,7 +754,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(vq::kThreads, 1)
       // ahead (four S buffers), so a slot is read before it is written again.
       const int slot = iter % kQSlots;
       mbar_wait(bar(kBarQScale + slot), static_cast<uint32_t>((iter / kQSlots) & 1), abort_flag);
-      const float row_scale = q_scale[slot * 64 + m] * p.scale_log2;
+      const float row_scale =
+          __uint_as_float(static_cast<uint32_t>(q_scale[slot * 64 + m]) << 16) * p.scale_log2;
       ++iter;
       float m_ref = -INFINITY;  // log2 units, page scale included
       float l_sum = 0.f;
@@ -757,93 +878,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(vq::kThreads, 1)
         named_barrier_sync(2, kSoftmaxThreads);
         if (t == 0) mbar_arrive_cluster(p_full_leader0 + 8u * pbuf);
       }
-      // ----------------------------------------------------------- epilogue
-      wait_o_through(G - 1);
-      red_l[part_of] = l_sum;
-      named_barrier_sync(1, kSoftmaxThreads);
-      const float l_row = (red_l[m] + red_l[64 + m]) + (red_l[128 + m] + red_l[192 + m]);
-      const bool empty_row = l_row == 0.f;
-      const float inv = empty_row ? 0.f : 1.f / l_row;
-      const float lse_nat = empty_row ? -INFINITY : (m_use - kBase + __log2f(l_row)) * kLn2;
-      uint8_t* stage = base + kOffP;
-      const uint32_t stage_addr = base_addr + kOffP;
-      if (!node_valid) {
-        // A node past q_len (odd q_len): nothing to write; release O.
-        tc_fence_before_sync();
-        named_barrier_sync(2, kSoftmaxThreads);
-        if (t == 0) mbar_arrive_cluster(o_free_leader);
-      } else if (!p.write_partials) {
-        const int row0 = (b * Q + node) * 64;
-#pragma unroll 1
-        for (int nh = 0; nh < 2; ++nh) {
-#pragma unroll 1
-          for (int q = 2 * g; q < 2 * g + 2; ++q) {
-            uint32_t o[32];
-            tmem_ld32(tmem + lane_addr + kTmemO + 128u * nh + 32u * q, o);
-            tmem_wait_ld();
-            // columns 256 nh + 128 hf + 32 q ..: 64-column box 2 hf + q / 2 of this half
-            uint8_t* rowp = stage + (2 * hf + (q >> 1)) * kBox + m * 128;
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-              uint32_t y[4];
-#pragma unroll
-              for (int z = 0; z < 4; ++z)
-                y[z] = pack_bf16x2(__uint_as_float(o[8 * v + 2 * z]) * inv,
-                                   __uint_as_float(o[8 * v + 2 * z + 1]) * inv);
-              *reinterpret_cast<uint4*>(rowp + (((4 * (q & 1) + v) ^ (m & 7)) << 4)) =
-                  make_uint4(y[0], y[1], y[2], y[3]);
-            }
-          }
-          if (nh == 1) tc_fence_before_sync();  // every read of O is done
-          fence_proxy_async_smem();
-          named_barrier_sync(2, kSoftmaxThreads);
-          if (nh == 1 && t == 0) mbar_arrive_cluster(o_free_leader);
-          if (t == 0) {
-            for (int c = 0; c < 4; ++c)
-              tma_store_3d(&tm_out, stage_addr + c * kBox, 256 * nh + 64 * c, row0, 0);
-            bulk_commit_group();
-            bulk_wait_group_read0();  // the staging buffer may be written again
-          }
-          named_barrier_sync(2, kSoftmaxThreads);
-        }
-        if (t < 64 && p.lse) p.lse[static_cast<int64_t>(row0) + m] = lse_nat;
-      } else {
-        // A split's normalised fp32 partial, in four rounds of 64 rows x 128 columns.
-        const int64_t rows_total = static_cast<int64_t>(p.B) * Q * 64;
-        const int64_t row0 = split * rows_total + (static_cast<int64_t>(b) * Q + node) * 64;
-#pragma unroll 1
-        for (int r = 0; r < 4; ++r) {
-          uint32_t o[32];
-          tmem_ld32(tmem + lane_addr + kTmemO + 128u * (r >> 1) + 32u * (2 * (r & 1) + g), o);
-          tmem_wait_ld();
-          uint8_t* rowp = stage + (2 * hf + g) * kBox + m * 128;
-#pragma unroll
-          for (int v = 0; v < 8; ++v)
-            *reinterpret_cast<float4*>(rowp + ((v ^ (m & 7)) << 4)) =
-                make_float4(__uint_as_float(o[4 * v]) * inv, __uint_as_float(o[4 * v + 1]) * inv,
-                            __uint_as_float(o[4 * v + 2]) * inv, __uint_as_float(o[4 * v + 3]) * inv);
-          if (r == 3) tc_fence_before_sync();
-          fence_proxy_async_smem();
-          named_barrier_sync(2, kSoftmaxThreads);
-          if (r == 3 && t == 0) mbar_arrive_cluster(o_free_leader);
-          if (t == 0) {
-            for (int c = 0; c < 4; ++c)
-              tma_store_3d(&tm_out, stage_addr + c * kBox,
-                           256 * (r >> 1) + 128 * (c >> 1) + 64 * (r & 1) + 32 * (c & 1),
-                           static_cast<int>(row0), 0);
-            bulk_commit_group();
-            bulk_wait_group_read0();
-          }
-          named_barrier_sync(2, kSoftmaxThreads);
-        }
-        if (t < 64) p.part_lse[row0 + m] = lse_nat;
-      }
+      // The row sums and their reference go to the output warps.
+      float* red = red_l + (iter - 1) % kLSlots * kRedL;
+      red[part_of] = l_sum;
+      if (t < 64) red[256 + m] = m_use;
+      mbar_arrive_local(bar(kBarL + (iter - 1) % kLSlots));
     }
-    if (t == 0) bulk_wait_group0();  // this CTA's output stores have completed
   }
 
-  // All MMAs of the pair are complete (the softmax warps waited for the last O, the
-  // issuers for their final commits); release tensor memory.
+  // All MMAs of the pair are complete (the output warps waited for the last O,
+  // the issuers for their final commits); release tensor memory.
   __syncwarp();
   tc_fence_before_sync();
   cluster_sync();
@@ -858,22 +902,17 @@ ddt_status launch_verify_attn_q8(const ddt_attn_q8_args& a, int num_splits, floa
   using namespace vq;
   const ddt_q8_cache& c = a.cache;
   const uint64_t pages = static_cast<uint64_t>(c.num_pages);
-  const uint64_t rows = static_cast<uint64_t>(a.B) * a.q_len * 64;
   const bool partials = num_splits > 1;
-  const uint64_t out_rows = partials ? rows * num_splits : rows;
   const int64_t items = static_cast<int64_t>(a.B) * ((a.q_len + 1) / 2) * num_splits;
-  if (items > 0x3fffffffll || out_rows > INT_MAX) return DDT_ERR_UNSUPPORTED;
+  if (items > 0x3fffffffll) return DDT_ERR_UNSUPPORTED;
   // With one page its stride is never taken, but the map wants one.
   const uint64_t lat_page = c.num_pages > 1 ? c.ckv_page_stride : kPage * c.ckv_row_stride;
   const uint64_t rope_page = c.num_pages > 1 ? c.kr_page_stride : kPage * c.kr_row_stride;
-  CUtensorMap m_lat, m_rope, m_out;
-  bool ok = make_map(&m_lat, c.c_kv, DDT_D_LATENT, kPage, pages, c.ckv_row_stride, lat_page, kPage,
+  CUtensorMap m_lat, m_rope;
+  const bool ok = make_map(&m_lat, c.c_kv, DDT_D_LATENT, kPage, pages, c.ckv_row_stride, lat_page, kPage,
                      CU_TENSOR_MAP_DATA_TYPE_UINT8, 128) &&
             make_map(&m_rope, c.k_rope, DDT_D_ROPE, kPage, pages, c.kr_row_stride, rope_page, kPage,
                      CU_TENSOR_MAP_DATA_TYPE_UINT8, 64, CU_TENSOR_MAP_SWIZZLE_64B);
-  ok = ok && (partials ? make_map(&m_out, part_o, 512, out_rows, 1, 512 * 4, out_rows * 512 * 4, 64,
-                                  CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 32)
-                       : make_map(&m_out, a.out, 512, out_rows, 1, 512 * 2, out_rows * 512 * 2, 64));
   if (!ok) return DDT_ERR_INVALID_ARG;
   if (ensure_smem_limit(reinterpret_cast<const void*>(verify_attn_q8_kernel), kSmemBytes, 6) !=
       cudaSuccess)
@@ -885,7 +924,9 @@ ddt_status launch_verify_attn_q8(const ddt_attn_q8_args& a, int num_splits, floa
   p.q_lat = static_cast<const uint16_t*>(a.q_lat);
   p.q_rope = static_cast<const uint16_t*>(a.q_rope);
   p.mask = a.mask;
+  p.out = static_cast<uint16_t*>(a.out);
   p.lse = a.lse;
+  p.part_o = part_o;
   p.part_lse = part_lse;
   p.status = a.status;
   p.B = a.B;
@@ -899,7 +940,7 @@ ddt_status launch_verify_attn_q8(const ddt_attn_q8_args& a, int num_splits, floa
   const int64_t slots = device_sm_count() / 2 > 0 ? device_sm_count() / 2 : 1;
   const int64_t grid = 2 * (items < slots ? items : slots);
   verify_attn_q8_kernel<<<static_cast<unsigned>(grid), kThreads, kSmemBytes, stream>>>(m_lat, m_rope,
-                                                                                      m_out, p);
+                                                                                      p);
   if (cudaGetLastError() != cudaSuccess) return DDT_ERR_CUDA;
   if (!partials) return DDT_OK;
   ddt_attn_args merge = {};
