@@ -580,7 +580,7 @@ DDT_API ddt_status ddt_kv_write_q8(const ddt_q8_cache* cache, const int32_t* pre
 /* ddt_verify_attn over the paged 8-bit cache: the same formula on the values that
  * the cache stands for, with the tree block at cache rows P .. P+q_len-1 (q_len 1
  * with mask word 1 is a plain decode step).  Queries are bf16 and enter as the sum
- * of two e4m3 terms under a power-of-two scale per row (exact to 2^-19 of the
+ * of two e4m3 terms under a power-of-two scale per row (exact to 2^-17 of the
  * row's largest value); softmax weights likewise (relative error at most 2^-8,
  * as a bf16 weight's); scores, sums and the output accumulate in fp32.
  *
@@ -590,7 +590,12 @@ DDT_API ddt_status ddt_kv_write_q8(const ddt_q8_cache* cache, const int32_t* pre
  * never read.  A NaN byte in a row of the request makes the whole request's
  * outputs NaN at that column, whether a node sees the row or not (0 * NaN);
  * ddt_kv_write_q8 never stores one.
- * Splits, workspace and max_prefix as for ddt_verify_attn.
+ * Splits: a request's cache may be cut into chunks whose partial results are merged.
+ * How many is decided on the device from the lengths themselves, at most
+ * ddt_verify_attn_q8_num_splits(args); num_splits > 0 forces that many for the longest
+ * request (and chunks of that size for the others).  It takes a workspace of
+ * ddt_verify_attn_q8_workspace_size(args) bytes, 256-byte aligned; with NULL or less no
+ * request is cut.  Calls that may overlap need workspaces of their own.
  * status int32 [B] or NULL: DDT_REQ_BAD_PREFIX (P < 0 or P + q_len > max_blocks *
  * 64), outputs of that request unwritten; DDT_REQ_BAD_INDEX (a page index of rows
  * < P + q_len): those rows count as zeros.
@@ -613,11 +618,11 @@ typedef struct ddt_attn_q8_args {
   size_t workspace_bytes;
   int32_t* status;    /* int32 [B] or NULL                                      */
   float softmax_scale; /* > 0 and finite                                        */
-  int32_t num_splits; /* 0 = choose automatically; otherwise 1..64              */
+  int32_t num_splits; /* 0 = choose on the device; otherwise 1..64              */
 } ddt_attn_q8_args;
 
-/* Bytes of workspace and number of KV splits the call will use (sizes only;
- * invalid sizes give 0 and 1). */
+/* Bytes of workspace, and the most KV splits the call may use (sizes only; invalid
+ * sizes give 0 and 1). */
 DDT_API size_t ddt_verify_attn_q8_workspace_size(const ddt_attn_q8_args* args);
 DDT_API int32_t ddt_verify_attn_q8_num_splits(const ddt_attn_q8_args* args);
 

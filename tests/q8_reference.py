@@ -179,9 +179,9 @@ def attend(query, cache, scales, table, P, vis, scale):
     out = (flat @ c).reshape(Q, HEADS, LATENT)
     mean = (flat @ np.abs(c)).reshape(Q, HEADS, LATENT)
     top_w = (p * step).max(2, keepdims=True)
-    quantum = 2.0 ** -16 * top_w * np.abs(raw[:, :LATENT]).sum(0)
+    quantum = 2.0 ** -14 * top_w * np.abs(raw[:, :LATENT]).sum(0)
     aq, ak = np.abs(query.reshape(-1, 576)), np.abs(key)
-    off = scale * (2.0 ** -19 * aq.max(1, keepdims=True) * ak.sum(1) + 640 * 2.0 ** -24 * (aq @ ak.T))
+    off = scale * (2.0 ** -17 * aq.max(1, keepdims=True) * ak.sum(1) + 640 * 2.0 ** -24 * (aq @ ak.T))
     off = (off.max(1) + 2.0 ** -20 * (1 + np.abs(s[np.isfinite(s)]).max(initial=0.0))).reshape(Q, HEADS)
     return out, lse, mean, quantum, off
 
@@ -189,8 +189,8 @@ def attend(query, cache, scales, table, P, vis, scale):
 def error_bound(out, mean, quantum, off):
     """How far the call's bf16 output may be from `out`.  Each weight enters P V as two
     e4m3 terms: relative error 2^-8, or, far below the largest one, 2^-10 where the
-    largest weight times its page's scale is at least 2^6 (the quantum term).  A score
-    that is off by `off` (queries in two e4m3 terms, 2^-19 of their row's largest value;
-    640 fp32 additions) changes weights by that factor, above and below the line.  The
+    largest weight times its page's scale is at least 2^4 (the quantum term).  A score
+    that is off by `off` (queries in two e4m3 terms: half a step, 2^-10, against a largest
+    value above 224 > 2^7; 640 fp32 additions) changes weights by that factor, above and below the line.  The
     result is rounded to bf16 once: 2^-8."""
     return (2.0 ** -8 + 2.0 * off[..., None]) * mean + quantum + 2.0 ** -8 * np.abs(out) + 1e-30

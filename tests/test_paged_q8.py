@@ -107,13 +107,20 @@ def test_other_refusals(lib):
     assert compact(B=0) == ddt.DDT_OK
 
 
-def test_split_plan_is_the_contiguous_call_s(lib):
-    for B, q, P in ((1, 33, 32768), (64, 33, 4096), (3, 1, 700), (1, 128, 0)):
-        a = attn_args(B=B, q_len=q, max_prefix=P, cache=good_cache(max_blocks=600))
-        plain = ddt.AttnArgs(B=B, q_len=q, num_heads=64, d_latent=512, d_rope=64, capacity=600 * 64, max_prefix=P)
-        assert lib.ddt_verify_attn_q8_num_splits(ctypes.byref(a)) == lib.ddt_verify_attn_num_splits(ctypes.byref(plain))
-        assert (lib.ddt_verify_attn_q8_workspace_size(ctypes.byref(a))
-                == lib.ddt_verify_attn_workspace_size(ctypes.byref(plain)))
+def test_split_bound_and_workspace(lib):
+    def of(**kw):
+        a = ctypes.byref(attn_args(cache=good_cache(max_blocks=600), **kw))
+        return lib.ddt_verify_attn_q8_num_splits(a), lib.ddt_verify_attn_q8_workspace_size(a)
+
+    assert of(B=64, q_len=33, max_prefix=4096) == (1, 0)         # enough items without cutting
+    for kw in (dict(B=1, q_len=33, max_prefix=32768), dict(B=64, q_len=1, max_prefix=4096), dict(B=1, q_len=9, max_prefix=256)):
+        s, ws = of(**kw)
+        tiles = -(-(kw["max_prefix"] + kw["q_len"]) // 128)
+        assert 1 < s <= min(32, tiles) and ws == 256 + s * kw["B"] * kw["q_len"] * 64 * 513 * 4
+    assert of(B=1, q_len=1, max_prefix=100)[0] == 1              # one tile
+    assert of(B=3, q_len=5, max_prefix=10, num_splits=7) == (7, 256 + 7 * 3 * 5 * 64 * 513 * 4)
+    assert of(B=513, q_len=1, max_prefix=4096, num_splits=4) == (1, 0)
+    assert of(B=0) == (1, 0) and of(q_len=0) == (1, 0)
 
 
 def test_binding_refuses_tensors_of_the_host():

@@ -438,7 +438,7 @@ ddt_status ddt_kv_compact_q8(const ddt_q8_cache* cache, const int32_t* prefix_le
   return DDT_OK;
 }
 
-// The sizes of a paged call in the form that the split plan takes.
+// The sizes of a paged call in the form that the shape checks take.
 static ddt_status q8_attn_shape(const ddt_attn_q8_args* a, ddt_attn_args* plain) {
   if (!a) return DDT_ERR_INVALID_ARG;
   if (a->cache.max_blocks < 0 || a->cache.max_blocks > kMaxBlocks) return DDT_ERR_INVALID_ARG;
@@ -457,13 +457,13 @@ static ddt_status q8_attn_shape(const ddt_attn_q8_args* a, ddt_attn_args* plain)
 int32_t ddt_verify_attn_q8_num_splits(const ddt_attn_q8_args* a) {
   ddt_attn_args plain;
   if (q8_attn_shape(a, &plain) != DDT_OK || plain.B == 0) return 1;
-  return verify_num_splits(plain, device_sm_count());
+  return q8_max_splits(*a, device_sm_count());
 }
 
 size_t ddt_verify_attn_q8_workspace_size(const ddt_attn_q8_args* a) {
   ddt_attn_args plain;
   if (q8_attn_shape(a, &plain) != DDT_OK || plain.B == 0) return 0;
-  return verify_workspace_bytes(plain, verify_num_splits(plain, device_sm_count()));
+  return q8_workspace_bytes(*a, q8_max_splits(*a, device_sm_count()));
 }
 
 ddt_status ddt_verify_attn_q8(const ddt_attn_q8_args* a, ddt_stream_t stream) {
@@ -476,21 +476,11 @@ ddt_status ddt_verify_attn_q8(const ddt_attn_q8_args* a, ddt_stream_t stream) {
     return DDT_ERR_INVALID_ARG;
   if (plain.capacity < a->q_len) return DDT_ERR_INVALID_ARG;
   if (!softmax_scale_ok(a->softmax_scale)) return DDT_ERR_INVALID_ARG;
-  int splits = verify_num_splits(plain, device_sm_count());
-  const size_t need = verify_workspace_bytes(plain, splits);
-  float* part_o = nullptr;
-  float* part_lse = nullptr;
-  if (splits > 1) {
-    if (!a->workspace || a->workspace_bytes < need ||
-        (reinterpret_cast<uintptr_t>(a->workspace) & 255u)) {
-      splits = 1;
-    } else {
-      part_o = static_cast<float*>(a->workspace);
-      part_lse = part_o + static_cast<size_t>(splits) * a->B * a->q_len * 64 * 512;
-    }
-  }
-  return launch_verify_attn_q8(*a, splits, part_o, part_lse,
-                               reinterpret_cast<cudaStream_t>(stream));
+  int splits = q8_max_splits(*a, device_sm_count());
+  if (splits > 1 && (!a->workspace || a->workspace_bytes < q8_workspace_bytes(*a, splits) ||
+                     (reinterpret_cast<uintptr_t>(a->workspace) & 255u)))
+    splits = 1;
+  return launch_verify_attn_q8(*a, splits, a->workspace, reinterpret_cast<cudaStream_t>(stream));
 }
 
 ddt_status ddt_decode_step(const ddt_decode_args* d, ddt_stream_t stream) {

@@ -69,11 +69,6 @@ ddt_status launch_verify_attn(const ddt_attn_args& a, int num_splits, float* par
 ddt_status launch_verify_attn_split_tail(const ddt_attn_args& a, int prefix_splits,
                                          float* part_o, float* part_lse, cudaStream_t stream);
 
-// Merge of num_partials split partials into out and lse (sizes of `a`; with `tail`
-// the last partial is the tree block's).
-ddt_status launch_verify_merge(const ddt_attn_args& a, int num_partials, int tail,
-                               const float* part_o, const float* part_lse, cudaStream_t stream);
-
 // The paged 8-bit cache.
 cudaError_t launch_kv_pages(const int32_t* prefix_lens, const int32_t* row_start, int B, int q_len,
                             int64_t n_rows, int num_pages, int max_blocks, int32_t* block_table,
@@ -89,8 +84,12 @@ cudaError_t launch_kv_compact_q8(const ddt_q8_cache& c, const int32_t* prefix_le
                                  const int32_t* path, const int32_t* accept_len, int B, int q_len,
                                  int32_t* new_prefix_lens, int32_t* status, cudaStream_t stream);
 
-ddt_status launch_verify_attn_q8(const ddt_attn_q8_args& a, int num_splits, float* part_o,
-                                 float* part_lse, cudaStream_t stream);
+// Most chunks that a paged verify call may cut a request into, the workspace for that
+// many, and the launch.
+int q8_max_splits(const ddt_attn_q8_args& a, int sm_count);
+size_t q8_workspace_bytes(const ddt_attn_q8_args& a, int max_splits);
+ddt_status launch_verify_attn_q8(const ddt_attn_q8_args& a, int max_splits, void* workspace,
+                                 cudaStream_t stream);
 
 // The fault word of the paged kernel (see ddt_fault_flags).
 cudaError_t q8_fault_flags(uint32_t* flags, bool reset);

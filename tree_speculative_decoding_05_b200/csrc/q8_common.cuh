@@ -6,14 +6,15 @@
 
 namespace ddt {
 
-// Larger of m and |x|, for each of two packed bf16 values; NaN if either is.
-__device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t m, uint32_t x) {
+// The larger magnitude of two packed bf16 values each, under some sign; NaN if either is.
+__device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
   uint32_t d;
-  asm("{\n\t.reg .b32 a;\n\tabs.bf16x2 a, %2;\n\tmax.NaN.bf16x2 %0, %1, a;\n\t}" : "=r"(d) : "r"(m), "r"(x));
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
 
-__device__ __forceinline__ uint32_t max_of_halves(uint32_t m) { return max(m & 0xffffu, m >> 16); }
+// The larger of the two halves' magnitudes.
+__device__ __forceinline__ uint32_t max_of_halves(uint32_t m) { return max(m & 0x7fffu, (m >> 16) & 0x7fffu); }
 
 // Smallest e with amax <= 448 * 2^e for the bits of a finite bf16 magnitude: 448 = 1.75 *
 // 2^8, so e is amax's exponent less 8, one more when its significand exceeds 1.75.

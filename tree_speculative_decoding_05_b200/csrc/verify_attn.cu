@@ -204,6 +204,14 @@ struct VerifyParams {
   int split_base;      // partial index of this launch's split 0
 };
 
+// KV tile range [t0, t1) of split `split` for a cache of T rows.
+__host__ __device__ inline void split_range(int T, int num_splits, int split, int& t0, int& t1) {
+  const int n_tiles = (T + kVerifyTileKeys - 1) / kVerifyTileKeys;
+  const int per = (n_tiles + num_splits - 1) / num_splits;
+  t0 = split * per;
+  t1 = t0 + per < n_tiles ? t0 + per : n_tiles;
+}
+
 // One work item: a pair of tree nodes of one request over one KV split.
 struct WorkItem {
   int b, pair, split, P, T, end, t0, ntile, last_tile;  // end: last row + 1 of this pass
@@ -993,10 +1001,8 @@ ddt_status launch_pass(const ddt_attn_args& a, int kv_mode, int num_splits, int 
   return cudaGetLastError() == cudaSuccess ? DDT_OK : DDT_ERR_CUDA;
 }
 
-}  // namespace
-
-ddt_status launch_verify_merge(const ddt_attn_args& a, int num_partials, int tail,
-                               const float* part_o, const float* part_lse, cudaStream_t stream) {
+ddt_status launch_merge(const ddt_attn_args& a, int num_partials, int tail, const float* part_o,
+                        const float* part_lse, cudaStream_t stream) {
   const int64_t rows = static_cast<int64_t>(a.B) * a.q_len * 64;
   verify_merge_kernel<<<static_cast<unsigned>((rows + 7) / 8), 256, 0, stream>>>(
       part_o, part_lse, a.prefix_lens, a.out, a.out_dtype == DDT_F32, a.lse, a.B, a.q_len,
@@ -1004,12 +1010,14 @@ ddt_status launch_verify_merge(const ddt_attn_args& a, int num_partials, int tai
   return cudaGetLastError() == cudaSuccess ? DDT_OK : DDT_ERR_CUDA;
 }
 
+}  // namespace
+
 ddt_status launch_verify_attn(const ddt_attn_args& a, int num_splits, float* part_o,
                               float* part_lse, cudaStream_t stream) {
   const ddt_status st =
       launch_pass(a, 0, num_splits, num_splits > 1, 0, part_o, part_lse, stream);
   if (st != DDT_OK || num_splits <= 1) return st;
-  return launch_verify_merge(a, num_splits, 0, part_o, part_lse, stream);
+  return launch_merge(a, num_splits, 0, part_o, part_lse, stream);
 }
 
 ddt_status launch_verify_attn_split_tail(const ddt_attn_args& a, int prefix_splits,
@@ -1018,7 +1026,7 @@ ddt_status launch_verify_attn_split_tail(const ddt_attn_args& a, int prefix_spli
   if (st != DDT_OK) return st;
   st = launch_pass(a, 2, 1, 1, prefix_splits, part_o, part_lse, stream);
   if (st != DDT_OK) return st;
-  return launch_verify_merge(a, prefix_splits + 1, 1, part_o, part_lse, stream);
+  return launch_merge(a, prefix_splits + 1, 1, part_o, part_lse, stream);
 }
 
 }  // namespace ddt

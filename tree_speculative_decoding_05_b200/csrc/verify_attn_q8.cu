@@ -41,10 +41,14 @@
 //     work, and then write this item's output while the softmax warps go on to the next.
 //   * S runs up to three tiles ahead of the softmax; O is rescaled only when the running
 //     maximum outgrows its reference by 2^2.75.
-//   * long caches: splits write normalised partials, merged by the bf16 call's merge.
+//   * work items are chunks of a request's tiles for a pair of nodes.  The host knows only
+//     a bound on the lengths, so the chunk is chosen on the device, by every CTA alike,
+//     from the lengths themselves (see make_plan); a request of one chunk is written
+//     directly, the others as normalised partials that a second kernel merges.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <climits>
 #include <cmath>
 #include <cstdint>
 
@@ -64,7 +68,6 @@ namespace ddt {
 namespace vq {
 constexpr int kPage = DDT_PAGE_ROWS;
 constexpr int kTK = 2 * kPage;  // keys per tile
-static_assert(kVerifyTileKeys % kTK == 0, "split ranges are whole tiles");
 constexpr int kWarpKProd0 = 8, kWarpSIss0 = 9, kWarpVProd = 10, kWarpPVIss = 11, kWarpKProd1 = 12,
               kWarpStatus = 13, kWarpSIss1 = 14, kWarpQ0 = 15;
 constexpr int kQWarps = 4;
@@ -81,9 +84,10 @@ constexpr int kKSlotBytes = 2 * kBox + kBox / 2;
 constexpr int kVSlots = 4;                     // 64 keys x 128 columns each
 constexpr int kPBufBytes = 2 * kBox;           // 64 rows x 128 keys: hi, lo
 constexpr int kPBufs = 2;
-constexpr int kLSlots = 4;                     // row sums of up to 4 items, see below
-constexpr int kQSlots = 8;                     // row scales of up to 8 items, see below
-constexpr int kMaxSortedB = 512;
+constexpr int kLSlots = 3;                     // row sums of up to 3 items, see below
+constexpr int kQSlots = 6;                     // row scales of up to 6 items, see below
+constexpr int kMaxSortedB = 512;                // requests that are put in order
+constexpr int kMaxSplitB = 128;                 // requests among which chunks are chosen
 constexpr int kOffQ = 0;
 constexpr int kOffKRing = kOffQ + kQBytes;
 constexpr int kOffVRing = kOffKRing + 2 * kKSlots * kKSlotBytes;
@@ -92,9 +96,11 @@ constexpr int kOffRedMax = kOffP + kPBufs * kPBufBytes;
 constexpr int kOffRedL = kOffRedMax + 2 * 256 * 4;  // red_max: float[2][4][64]
 constexpr int kRedL = 5 * 64;                       // red_l: four parts of each row sum, its maximum
 constexpr int kOffQScale = kOffRedL + kLSlots * kRedL * 4;  // bf16[kQSlots][64]
-constexpr int kOffOrder = kOffQScale + kQSlots * 64 * 2;  // uint16[kMaxSortedB]
-constexpr int kOffBar = kOffOrder + kMaxSortedB * 2;
-constexpr int kOffLen = kOffP;  // int[kMaxSortedB], before the first tile
+constexpr int kOffOrder = kOffQScale + kQSlots * 64 * 2;  // uint16[2][kMaxSortedB], see Plan
+constexpr int kOffStarts = kOffOrder + 2 * kMaxSortedB * 2;  // uint16[kMaxSortedB + 2]
+constexpr int kOffPlan = kOffStarts + (kMaxSortedB + 2) * 2;  // int[4]
+constexpr int kOffBar = (kOffPlan + 4 * 4 + 7) / 8 * 8;
+constexpr int kOffTiles = kOffP;  // before the first tile: what the plan is made from
 constexpr int kBarKFull = 0;  // ring g at g * kKSlots
 constexpr int kBarKEmpty = kBarKFull + 2 * kKSlots;
 constexpr int kBarVFull = kBarKEmpty + 2 * kKSlots;
@@ -116,14 +122,18 @@ constexpr int kOffAbort = kOffTmemPtr + 4;
 constexpr int kSmemUsed = kOffAbort + 4;
 constexpr int kSmemBytes = kSmemUsed + 1024;  // slack for 1024-byte alignment
 static_assert(kSmemBytes <= 232448, "shared memory budget");
+static_assert((2 * kMaxSortedB + 64 + kThreads / 32 * (kMaxSplitB / 2 * 3)) * 4 <= kPBufs * kPBufBytes, "plan");
 
 constexpr int kTmemCols = 512, kTmemS = 0, kTmemO = 256;
 constexpr uint32_t kIdescQK = idesc_e4m3_f32(128, kTK, false);
 constexpr uint32_t kIdescPV = idesc_e4m3_f32(128, 256, true);
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // The reference weight 2^kBase and the growth kSlack allowed before O is rescaled:
-// 2^(6 + 2.75) = 431 <= 448.
-constexpr float kBase = 6.0f, kSlack = 2.75f;
+// 2^(4 + 4.75) = 431 <= 448.  Rescaling costs a wait for P V and a pass over O, and any
+// row of a warp's 32 causes it: for normally distributed scores (deviation 1.7) two rows
+// in five outgrow 2^2.75 between the first tile and the 33rd, one in thirty 2^4.75.  The
+// steps at the bottom are then 2^-13 of the largest weight.
+constexpr float kBase = 4.0f, kSlack = 4.75f;
 constexpr float kMinScale = 9.094947017729282e-13f;  // 2^-40
 
 struct Params {
@@ -138,39 +148,107 @@ struct Params {
   float* part_o;    // [num_splits][B * Q * 64][512]
   float* part_lse;  // [num_splits][B * Q * 64]
   int32_t* status;
-  int B, Q, num_pages, max_blocks, num_splits, n_pairs, write_partials;
+  int32_t* chunk;   // the chunk chosen, for the merge
+  int B, Q, num_pages, max_blocks, n_pairs;
+  int max_splits;   // most chunks of a request that the partials have room for
+  int forced;       // cut the longest request into max_splits chunks
   float scale_log2;  // softmax_scale * log2(e)
+};
+
+// The work list: first all whole chunks, requests by decreasing length (`order`; starts
+// counts the chunks before a request's), then the remainders by decreasing size (order
+// + kMaxSortedB).  Consecutive items are the node pairs of one chunk, which share its
+// rows in the L2.
+struct Plan {
+  const uint16_t* order;  // null: requests as they come, one chunk each
+  const uint16_t* starts;
+  int chunk, full, n_items;  // tiles of a whole chunk; items that are whole chunks; all items
 };
 
 struct Item {
   int b, pair, split, P, T, t0, ntile;
-  bool bad_prefix, valid;
+  bool single, valid;  // single: the request's only chunk
 };
 
-__device__ __forceinline__ Item decode_item(const Params& p, int w, const uint16_t* order) {
+// A request's tiles; 0 for one whose rows do not fit its table.
+__device__ __forceinline__ int tiles_of(const Params& p, int P) {
+  if (P < 0 || static_cast<int64_t>(P) + p.Q > static_cast<int64_t>(p.max_blocks) * kPage) return 0;
+  return (P + p.Q + kTK - 1) / kTK;
+}
+
+__device__ __forceinline__ Item decode_item(const Params& p, int w, const Plan& plan) {
   Item it;
-  const int per_req = p.n_pairs * p.num_splits;
-  const int slot = w / per_req;
-  it.b = order ? order[slot] : slot;
-  const int rem = w - slot * per_req;
-  it.pair = rem / p.num_splits;
-  it.split = rem - it.pair * p.num_splits;
-  it.P = p.prefix_lens[it.b];
-  it.bad_prefix = it.P < 0 || static_cast<int64_t>(it.P) + p.Q >
-                                  static_cast<int64_t>(p.max_blocks) * kPage;
-  it.T = it.P + p.Q;
-  int t0 = 0, t1 = 0;
-  if (!it.bad_prefix) {
-    constexpr int kUnit = kVerifyTileKeys / kTK;
-    split_range(it.T, p.num_splits, it.split, t0, t1);
-    const int n = (it.T + kTK - 1) / kTK;
-    t0 *= kUnit;
-    t1 = t1 * kUnit < n ? t1 * kUnit : n;
+  const bool whole = w < plan.full;
+  const int v = whole ? w : w - plan.full;
+  const int u = v / p.n_pairs;
+  it.pair = v - u * p.n_pairs;
+  it.split = 0;
+  if (!plan.order) {
+    it.b = u;
+  } else if (whole) {
+    int lo = 0, hi = p.B;  // the last request with starts <= u
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (plan.starts[mid] <= u) lo = mid;
+      else hi = mid;
+    }
+    it.b = plan.order[lo];
+    it.split = u - plan.starts[lo];
+  } else {
+    it.b = plan.order[kMaxSortedB + u];
   }
-  it.t0 = t0;
-  it.ntile = t1 - t0;
-  it.valid = !it.bad_prefix && it.ntile > 0;
+  it.P = p.prefix_lens[it.b];
+  it.T = it.P + p.Q;
+  const int n = tiles_of(p, it.P);
+  const int chunks = n / plan.chunk, rest = n - chunks * plan.chunk;
+  if (!whole) it.split = chunks;
+  it.t0 = it.split * plan.chunk;
+  it.ntile = whole ? plan.chunk : rest;
+  it.single = chunks + (rest > 0) == 1;
+  it.valid = it.ntile > 0;
   return it;
+}
+
+// What a choice of chunk costs, in tiles: the longest of the pairs' shares under the
+// schedule that work_index gives, each item counting kItemTiles on top of its tiles
+// (queries, filling and draining the pipeline), and the merge.  By one warp, for requests
+// of tiles[0 .. B); `sorted` has room for 3/2 kMaxSplitB numbers.
+constexpr float kItemTiles = 4.5f, kMergeTiles = 3.f;
+__device__ float plan_cost(const int* tiles, int B, int n_pairs, int n_clusters, int chunk,
+                           int* sorted) {
+  const int lane = threadIdx.x & 31;
+  int whole = 0, rests = 0;
+  int* key = sorted + kMaxSplitB / 2;  // rest and index in one, so that all differ
+  for (int b = lane; b < B; b += 32) {
+    const int n = tiles[b] / chunk, rest = tiles[b] - n * chunk;
+    whole += n;
+    rests += rest > 0;
+    key[b] = rest * kMaxSplitB + b;
+  }
+  __syncwarp();
+  uint16_t* order = reinterpret_cast<uint16_t*>(sorted);
+  for (int b = lane; b < B; b += 32) {
+    const int mine = key[b];
+    int rank = 0;
+#pragma unroll 8
+    for (int i = 0; i < B; ++i) rank += key[i] > mine;
+    order[rank] = static_cast<uint16_t>(mine / kMaxSplitB);
+  }
+  whole = __reduce_add_sync(0xffffffffu, whole) * n_pairs;
+  const int n = whole + __reduce_add_sync(0xffffffffu, rests) * n_pairs;
+  __syncwarp();
+  float most = 0.f;
+  for (int j = lane; j < n_clusters; j += 32) {
+    float share = 0.f;
+    for (int k = 0; k * n_clusters < n; ++k) {
+      const int w = work_index(k, j, n_clusters, n);
+      if (w >= 0) share += kItemTiles + (w < whole ? chunk : order[n_pairs == 1 ? w - whole : (w - whole) / n_pairs]);
+    }
+    most = fmaxf(most, share);
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
+  return most;
 }
 
 // A block of the cache (64 rows): its page, -1 for none, and how many of its rows the
@@ -211,26 +289,32 @@ __device__ __forceinline__ uint32_t pack16(uint16_t lo, uint16_t hi) {
   return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
 }
 
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
 // One query row, by a warp: a lane has latent values 16 lane .. + 15 (x[0 .. 7]) and rope
 // values 2 lane, 2 lane + 1 (x[8]).
 __device__ __forceinline__ void split_row(const uint32_t (&x)[9], uint8_t* q, int row, int lane,
                                           uint16_t* scale) {
-  uint32_t m = 0;
+  uint32_t m = x[0];
 #pragma unroll
-  for (int j = 0; j < 9; ++j) m = max_abs_bf16x2(m, x[j]);
+  for (int j = 1; j < 9; ++j) m = max_abs_bf16x2(m, x[j]);
   const uint32_t top = __reduce_max_sync(0xffffffffu, max_of_halves(m));
   int e = e4m3_exponent(top);
   e = top == 0 ? 0 : e < -100 ? -100 : e;
-  const float inv = pow2f(-e);
+  // a power of two: exact in bf16 (down to its subnormals, far below e4m3's steps)
+  const uint32_t inv = static_cast<uint32_t>(127 - e) << 7 | static_cast<uint32_t>(127 - e) << 23;
   uint32_t hi[5], lo[5];
 #pragma unroll
   for (int j = 0; j < 5; ++j) {
     uint16_t f[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int v = 0; v < (j < 4 ? 2 : 1); ++v) {
-      const uint32_t h = x[2 * j + v];
-      split_e4m3x2(__uint_as_float(h << 16) * inv, __uint_as_float(h & 0xffff0000u) * inv, f[v],
-                   f[2 + v]);
+      const uint32_t h = mul_bf16x2(x[2 * j + v], inv);
+      split_e4m3x2(__uint_as_float(h << 16), __uint_as_float(h & 0xffff0000u), f[v], f[2 + v]);
     }
     hi[j] = pack16(f[0], f[1]);
     lo[j] = pack16(f[2], f[3]);
@@ -268,8 +352,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(vq::kThreads, 1)
   const uint32_t rank = cluster_ctarank();
   const int cluster = static_cast<int>(blockIdx.x >> 1);
   const int n_clusters = static_cast<int>(gridDim.x >> 1);
-  const int n_items = p.B * p.n_pairs * p.num_splits;
-  const int n_rounds = (n_items + n_clusters - 1) / n_clusters;
   const int Q = p.Q;
 
   extern __shared__ uint8_t smem_raw[];
@@ -319,38 +401,93 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(vq::kThreads, 1)
     tmem_alloc<2>(smem_u32(tmem_ptr_smem), kTmemCols);
     tmem_relinquish<2>();
   }
-  // Requests by decreasing length (ties by index), found by every CTA for itself; equal
-  // lengths need no look at each other.
-  int* len_smem = reinterpret_cast<int*>(base + kOffLen);
-  uint16_t* order_smem = reinterpret_cast<uint16_t*>(base + kOffOrder);
-  const bool sorted = p.B <= kMaxSortedB;
-  if (sorted) {
-    int differs = 0;
-    for (int b = threadIdx.x; b < p.B; b += kThreads) {
-      const int P = p.prefix_lens[b];
-      len_smem[b] = P < 0 || static_cast<int64_t>(P) + Q > static_cast<int64_t>(p.max_blocks) * kPage
-                        ? 0 : P + Q;
-      differs |= P != p.prefix_lens[0];
+  // The plan, made by every CTA for itself.
+  int* const plan_smem = reinterpret_cast<int*>(base + kOffPlan);  // longest, shortest, whole chunks
+  Plan plan = {nullptr, nullptr, INT_MAX, 0, p.B * p.n_pairs};
+  if (p.B <= kMaxSortedB) {
+    int* tiles = reinterpret_cast<int*>(base + kOffTiles);
+    int* rests = tiles + kMaxSortedB;
+    float* costs = reinterpret_cast<float*>(rests + kMaxSortedB);  // [64]
+    int* sorted = rests + kMaxSortedB + 64;                        // of each warp
+    uint16_t* order = reinterpret_cast<uint16_t*>(base + kOffOrder);
+    uint16_t* starts = reinterpret_cast<uint16_t*>(base + kOffStarts);
+    plan.order = order;
+    plan.starts = starts;
+    const int mine = threadIdx.x < p.B ? tiles_of(p, p.prefix_lens[threadIdx.x]) : 0;
+    if (threadIdx.x == 0) {
+      plan_smem[0] = 1;
+      plan_smem[1] = INT_MAX;
     }
-    differs = __syncthreads_or(differs);
-    for (int bi = threadIdx.x; bi < p.B; bi += kThreads) {
-      const int li = len_smem[bi];
-      int before = differs ? 0 : bi;
+    __syncthreads();
+    if (threadIdx.x < p.B) {
+      tiles[threadIdx.x] = mine;
+      atomicMax(&plan_smem[0], mine);
+      atomicMin(&plan_smem[1], mine);
+    }
+    __syncthreads();
+    const int longest = plan_smem[0];
+    const bool differs = plan_smem[1] != longest;
+    plan.chunk = p.forced ? (longest + p.max_splits - 1) / p.max_splits : longest;
+    if (p.max_splits > 1 && !p.forced) {
+      // one warp prices one number of chunks for the longest request
+      const int most = p.max_splits < longest ? p.max_splits : longest;
+      for (int c = warp + 1; c <= most; c += kThreads / 32) {
+        const float cost = plan_cost(tiles, p.B, p.n_pairs, n_clusters, (longest + c - 1) / c,
+                                     sorted + warp * (kMaxSplitB / 2 * 3));
+        if (lane == 0) costs[c - 1] = c > 1 ? cost + kMergeTiles : cost;
+      }
+      __syncthreads();
+      int best = 1;
+      for (int c = 2; c <= most; ++c)
+        if (costs[c - 1] < costs[best - 1]) best = c;
+      plan.chunk = (longest + best - 1) / best;
+    }
+    const int rest = mine % plan.chunk;
+    if (threadIdx.x < p.B) rests[threadIdx.x] = rest;
+    const int n_rests = __syncthreads_count(rest > 0);
+    if (threadIdx.x < p.B) {
+      int before = threadIdx.x, before_rest = threadIdx.x;
       if (differs) {
-#pragma unroll 8
-        for (int bj = 0; bj < p.B; ++bj) {
-          const int lj = len_smem[bj];
-          before += lj > li || (lj == li && bj < bi);
+        before = before_rest = 0;
+        const int i = threadIdx.x;
+#pragma unroll 4
+        for (int j = 0; j < p.B; ++j) {
+          const int tj = tiles[j], rj = rests[j];
+          before += tj > mine || (tj == mine && j < i);
+          before_rest += rj > rest || (rj == rest && j < i);
         }
       }
-      order_smem[before] = static_cast<uint16_t>(bi);
+      order[before] = static_cast<uint16_t>(threadIdx.x);
+      order[kMaxSortedB + before_rest] = static_cast<uint16_t>(threadIdx.x);
     }
+    __syncthreads();
+    if (warp == 0) {
+      int sum = 0;
+      for (int r0 = 0; r0 < p.B; r0 += 32) {
+        const int r = r0 + lane;
+        const int whole = r < p.B ? tiles[order[r]] / plan.chunk : 0;
+        int upto = whole;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+          const int o = __shfl_up_sync(0xffffffffu, upto, off);
+          if (lane >= off) upto += o;
+        }
+        if (r < p.B) starts[r] = static_cast<uint16_t>(sum + upto - whole);
+        sum += __shfl_sync(0xffffffffu, upto, 31);
+      }
+      if (lane == 0) plan_smem[2] = sum;
+    }
+    __syncthreads();
+    plan.full = plan_smem[2] * p.n_pairs;
+    plan.n_items = plan.full + n_rests * p.n_pairs;
+    if (p.max_splits > 1 && blockIdx.x == 0 && threadIdx.x == 0) *p.chunk = plan.chunk;
   }
+  const int n_items = plan.n_items;
+  const int n_rounds = (n_items + n_clusters - 1) / n_clusters;
   tc_fence_before_sync();
   cluster_sync();
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_ptr_smem;
-  const uint16_t* order = sorted ? order_smem : nullptr;
 
   struct Ring {
     int stage = 0;
@@ -363,6 +500,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(vq::kThreads, 1)
     }
   };
   const bool leader = rank == 0;
+  // Rows r .. r + 3 of this CTA's node of item `it`, split by one warp.
+  auto split_rows = [&](const Item& it, int r, int iter) {
+    const int node = 2 * it.pair + static_cast<int>(rank);
+    const int64_t row0 = (static_cast<int64_t>(it.b) * Q + node) * 64 + r;
+    const uint4* lat = reinterpret_cast<const uint4*>(p.q_lat) + row0 * 64 + 2 * lane;
+    const uint32_t* rope = reinterpret_cast<const uint32_t*>(p.q_rope) + row0 * 32 + lane;
+    uint32_t x[4][9];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint4 a = make_uint4(0, 0, 0, 0), c = a;
+      x[i][8] = 0;
+      if (node < Q) {
+        a = lat[i * 64];
+        c = lat[i * 64 + 1];
+        x[i][8] = rope[i * 32];
+      }
+      x[i][0] = a.x, x[i][1] = a.y, x[i][2] = a.z, x[i][3] = a.w;
+      x[i][4] = c.x, x[i][5] = c.y, x[i][6] = c.z, x[i][7] = c.w;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      split_row(x[i], base + kOffQ, r + i, lane, q_scale + iter % kQSlots * 64);
+  };
   const int ring_g = warp == kWarpKProd1 || warp == kWarpSIss1 ? 1 : 0;
 
   if (warp == kWarpKProd0 || warp == kWarpKProd1) {
@@ -376,7 +536,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(vq::kThreads, 1)
       for (int k = 0; k < n_rounds; ++k) {
         const int w = work_index(k, cluster, n_clusters, n_items);
         if (w < 0) continue;
-        const Item it = decode_item(p, w, order);
+        const Item it = decode_item(p, w, plan);
         if (!it.valid) continue;
         // tiles of this ring, the page number of the next one loaded ahead of the wait
         int jj = static_cast<int>(G & 1) == g ? 0 : 1;
@@ -408,7 +568,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(vq::kThreads, 1)
       for (int k = 0; k < n_rounds; ++k) {
         const int w = work_index(k, cluster, n_clusters, n_items);
         if (w < 0) continue;
-        const Item it = decode_item(p, w, order);
+        const Item it = decode_item(p, w, plan);
         if (!it.valid) continue;
         const int blk0 = 2 * it.t0, n_blk = 2 * it.ntile;
         Block next = load_block(p, it, blk0);
@@ -447,7 +607,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(vq::kThreads, 1)
       for (int k = 0; k < n_rounds; ++k) {
         const int w = work_index(k, cluster, n_clusters, n_items);
         if (w < 0) continue;
-        const Item it = decode_item(p, w, order);
+        const Item it = decode_item(p, w, plan);
         if (!it.valid) continue;
         mbar_wait(bar(kBarQ), static_cast<uint32_t>(iter & 1), abort_flag);
         for (int jj = 0; jj < it.ntile; ++jj, ++G) {
@@ -503,7 +663,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(vq::kThreads, 1)
       for (int k = 0; k < n_rounds; ++k) {
         const int w = work_index(k, cluster, n_clusters, n_items);
         if (w < 0) continue;
-        const Item it = decode_item(p, w, order);
+        const Item it = decode_item(p, w, plan);
         if (!it.valid) continue;
         if (iter > 0) {  // both CTAs' output warps have read the previous item's O
           mbar_wait(bar(kBarOFree), static_cast<uint32_t>((iter - 1) & 1), abort_flag);
@@ -547,34 +707,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(vq::kThreads, 1)
     auto split_queries = [&](const Item& it, int iter) {
       const int node = 2 * it.pair + static_cast<int>(rank);
       const int64_t row0 = (static_cast<int64_t>(it.b) * Q + node) * 64 + 16 * u;
-      const uint4* lat = reinterpret_cast<const uint4*>(p.q_lat) + row0 * 64 + 2 * lane;
-      const uint32_t* rope = reinterpret_cast<const uint32_t*>(p.q_rope) + row0 * 32 + lane;
-      uint16_t* scale = q_scale + iter % kQSlots * 64;
-      if (node < Q) {  // 16 rows of 1024 and of 128 bytes, one line a lane
+      if (node < Q) {  // rows of 1024 and of 128 bytes, one line a lane
 #pragma unroll
         for (int i = 0; i < 4; ++i) prefetch_l2(p.q_lat + row0 * 512 + (32 * i + lane) * 64);
         if (lane < 16) prefetch_l2(p.q_rope + row0 * 64 + lane * 64);
       }
+      if (iter > 0)
+        mbar_wait(bar(kBarQFree), static_cast<uint32_t>((iter - 1) & 1), abort_flag);
 #pragma unroll 1
-      for (int r0 = 0; r0 < 16; r0 += 4) {
-        uint32_t x[4][9];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          uint4 a = make_uint4(0, 0, 0, 0), c = a;
-          x[r][8] = 0;
-          if (node < Q) {
-            a = lat[(r0 + r) * 64];
-            c = lat[(r0 + r) * 64 + 1];
-            x[r][8] = rope[(r0 + r) * 32];
-          }
-          x[r][0] = a.x, x[r][1] = a.y, x[r][2] = a.z, x[r][3] = a.w;
-          x[r][4] = c.x, x[r][5] = c.y, x[r][6] = c.z, x[r][7] = c.w;
-        }
-        if (r0 == 0 && iter > 0)
-          mbar_wait(bar(kBarQFree), static_cast<uint32_t>((iter - 1) & 1), abort_flag);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) split_row(x[r], base + kOffQ, 16 * u + r0 + r, lane, scale);
-      }
+      for (int r = 16 * u; r < 16 * u + 16; r += 4) split_rows(it, r, iter);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
@@ -587,7 +728,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(vq::kThreads, 1)
       for (; k < n_rounds; ++k) {
         const int w = work_index(k, cluster, n_clusters, n_items);
         if (w < 0) continue;
-        it = decode_item(p, w, order);
+        it = decode_item(p, w, plan);
         if (it.valid) {
           ++k;
           return true;
@@ -605,8 +746,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(vq::kThreads, 1)
     for (int iter = 0; have; ++iter) {
       const bool more = next_item(nxt);
       if (more) split_queries(nxt, iter + 1);
-      // The row sums of item i lie in slot i % 4: softmax is at most three items ahead
-      // of the output (two P buffers, and P V of item i + 1 waits for item i's output).
+      // The row sums of item i lie in slot i % 3: the softmax of item j is done only once
+      // the output of item j - 3 is (two P buffers, and the P V of an item waits for the
+      // output of the one before).
       G += cur.ntile;
       const float* red = red_l + iter % kLSlots * kRedL;
       mbar_wait(bar(kBarL + iter % kLSlots), static_cast<uint32_t>((iter / kLSlots) & 1), abort_flag);
@@ -620,22 +762,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(vq::kThreads, 1)
       mbar_wait(bar(kBarO + static_cast<int>((G - 1) & 3)), static_cast<uint32_t>(((G - 1) >> 2) & 1),
                 abort_flag);
       tc_fence_after_sync();
-      // Lane t has columns 256 nh + 128 hf + 0 .. 127 of its row; 32 at a time, each a
-      // run of whole 32-byte sectors.
+      // Lane t has columns 256 nh + 128 hf + 0 .. 127 of its row; 32 at a time, in runs
+      // of whole 32-byte sectors.
       if (node < Q) {
-        if (!p.write_partials) {
-          uint16_t* out = p.out + row * DDT_D_LATENT + 128 * hf;
-#pragma unroll 2
-          for (int q = 0; q < 8; ++q) {
-            uint32_t o[32];
-            tmem_ld32(tmem + lane_addr + kTmemO + 32u * q, o);
-            tmem_wait_ld();
-            if (q == 7) {
-              tc_fence_before_sync();
-              __syncwarp();
-              if (lane == 0) mbar_arrive_cluster(o_free_leader);
-            }
-            uint16_t* at = out + 256 * (q >> 2) + 32 * (q & 3);
+        const int64_t prow = cur.split * static_cast<int64_t>(p.B) * Q * 64 + row;
+        uint16_t* out = p.out + row * DDT_D_LATENT + 128 * hf;
+        float* part = p.part_o + prow * DDT_D_LATENT + 128 * hf;
+#pragma unroll 1
+        for (int q = 0; q < 8; ++q) {
+          uint32_t o[32];
+          tmem_ld32(tmem + lane_addr + kTmemO + 32u * q, o);
+          tmem_wait_ld();
+          if (q == 7) {
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(o_free_leader);
+          }
+          const int col = 256 * (q >> 2) + 32 * (q & 3);
+          if (cur.single) {
 #pragma unroll
             for (int v = 0; v < 2; ++v) {
               uint32_t y[8];
@@ -643,33 +787,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(vq::kThreads, 1)
               for (int z = 0; z < 8; ++z)
                 y[z] = pack_bf16x2(__uint_as_float(o[16 * v + 2 * z]) * inv,
                                    __uint_as_float(o[16 * v + 2 * z + 1]) * inv);
-              store_sector(at + 16 * v, y);
+              store_sector(out + col + 16 * v, y);
             }
-          }
-          if (hf == 0 && p.lse) p.lse[row] = lse_nat;
-        } else {  // a split's normalised fp32 partial
-          const int64_t prow = cur.split * static_cast<int64_t>(p.B) * Q * 64 + row;
-          float* out = p.part_o + prow * DDT_D_LATENT + 128 * hf;
-#pragma unroll 2
-          for (int q = 0; q < 8; ++q) {
-            uint32_t o[32];
-            tmem_ld32(tmem + lane_addr + kTmemO + 32u * q, o);
-            tmem_wait_ld();
-            if (q == 7) {
-              tc_fence_before_sync();
-              __syncwarp();
-              if (lane == 0) mbar_arrive_cluster(o_free_leader);
-            }
-            float* at = out + 256 * (q >> 2) + 32 * (q & 3);
+          } else {  // a chunk's normalised fp32 partial
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
               uint32_t y[8];
 #pragma unroll
               for (int z = 0; z < 8; ++z) y[z] = __float_as_uint(__uint_as_float(o[8 * v + z]) * inv);
-              store_sector(at + 8 * v, y);
+              store_sector(part + col + 8 * v, y);
             }
           }
-          if (hf == 0) p.part_lse[prow] = lse_nat;
+        }
+        if (hf == 0) {
+          if (!cur.single) p.part_lse[prow] = lse_nat;
+          else if (p.lse) p.lse[row] = lse_nat;
         }
       } else {  // a node past q_len (odd q_len): nothing to write
         tc_fence_before_sync();
@@ -680,24 +812,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(vq::kThreads, 1)
       have = more;
     }
   } else if (warp == kWarpStatus) {
-    // A request's status, by the even CTA that has its first pair and split: whether
-    // its prefix fits and all its page numbers are some.
+    // Every request's status, by one even CTA: whether its prefix fits and all its page
+    // numbers are some.
     if (leader && p.status) {
-      for (int k = 0; k < n_rounds; ++k) {
-        const int w = work_index(k, cluster, n_clusters, n_items);
-        if (w < 0) continue;
-        const Item it = decode_item(p, w, order);
-        if (it.pair != 0 || it.split != 0) continue;
-        int st = it.bad_prefix ? DDT_REQ_BAD_PREFIX : DDT_REQ_OK;
-        if (!it.bad_prefix) {
+      for (int b = cluster; b < p.B; b += n_clusters) {
+        const int P = p.prefix_lens[b];
+        int st = DDT_REQ_OK;
+        if (tiles_of(p, P) == 0) {
+          st = DDT_REQ_BAD_PREFIX;
+        } else {
           bool bad = false;
-          for (int blk = lane; blk * kPage < it.T; blk += 32) {
-            const int page = p.block_table[static_cast<int64_t>(it.b) * p.max_blocks + blk];
+          for (int blk = lane; blk * kPage < P + Q; blk += 32) {
+            const int page = p.block_table[static_cast<int64_t>(b) * p.max_blocks + blk];
             bad |= page < 0 || page >= p.num_pages;
           }
           if (__any_sync(0xffffffffu, bad)) st = DDT_REQ_BAD_INDEX;
         }
-        if (lane == 0) p.status[it.b] = st;
+        if (lane == 0) p.status[b] = st;
       }
     }
   } else {
@@ -730,7 +861,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(vq::kThreads, 1)
     for (int k = 0; k < n_rounds; ++k) {
       const int w = work_index(k, cluster, n_clusters, n_items);
       if (w < 0) continue;
-      const Item it = decode_item(p, w, order);
+      const Item it = decode_item(p, w, plan);
       if (!it.valid) continue;
       const int b = it.b, P = it.P;
       const int node = 2 * it.pair + static_cast<int>(rank);
@@ -750,8 +881,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(vq::kThreads, 1)
       const int blk0 = 2 * it.t0 + hf;
       Block cur = load_block(p, it, blk0), nxt = load_block(p, it, blk0 + 2);
       float ks_next = page_scale(cur);
-      // The row scales of item i lie in slot i % 8: queries run at most five items
-      // ahead (four S buffers), so a slot is read before it is written again.
+      // The row scales of item i lie in slot i % 6: queries run at most five items ahead
+      // (four S buffers), so a slot is read before it is written again.
       const int slot = iter % kQSlots;
       mbar_wait(bar(kBarQScale + slot), static_cast<uint32_t>((iter / kQSlots) & 1), abort_flag);
       const float row_scale =
@@ -897,22 +1028,104 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(vq::kThreads, 1)
   }
 }
 
-ddt_status launch_verify_attn_q8(const ddt_attn_q8_args& a, int num_splits, float* part_o,
-                                 float* part_lse, cudaStream_t stream) {
+// One warp per output row: lse = ln sum_s exp(lse_s), out = sum_s exp(lse_s - lse) out_s
+// over the chunks of a request that has several; the others have been written.
+__global__ void __launch_bounds__(256) verify_merge_q8_kernel(
+    const float* __restrict__ part_o, const float* __restrict__ part_lse,
+    const int32_t* __restrict__ chunk, const int32_t* __restrict__ prefix_lens,
+    uint16_t* __restrict__ out, float* __restrict__ lse, int B, int Q, int max_blocks) {
+  const int64_t rows_total = static_cast<int64_t>(B) * Q * 64;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (row >= rows_total) return;
+  const int c = *chunk;
+  const int P = prefix_lens[row / (static_cast<int64_t>(Q) * 64)];
+  if (P < 0 || static_cast<int64_t>(P) + Q > static_cast<int64_t>(max_blocks) * vq::kPage) return;
+  const int n = ((P + Q + vq::kTK - 1) / vq::kTK + c - 1) / c;  // at most 64
+  if (n <= 1) return;
+  const float l0 = lane < n ? part_lse[lane * rows_total + row] : -INFINITY;
+  const float l1 = lane + 32 < n ? part_lse[(lane + 32) * rows_total + row] : -INFINITY;
+  float top = fmaxf(l0, l1);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+  // NaN stays NaN; a row that sees no key in any chunk has sum 0
+  const float ref = top == -INFINITY ? 0.f : top;
+  const float w0 = l0 == -INFINITY ? 0.f : fast_exp2((l0 - ref) * vq::kLog2e);
+  const float w1 = l1 == -INFINITY ? 0.f : fast_exp2((l1 - ref) * vq::kLog2e);
+  float sum = w0 + w1;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+  float acc[16];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) acc[k] = 0.f;
+  for (int s0 = 0; s0 < n; s0 += 4) {  // four partial rows in flight
+    float4 v[4][4];
+    float w[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int sp = s0 + u;
+      const float a = __shfl_sync(0xffffffffu, w0, sp & 31), b = __shfl_sync(0xffffffffu, w1, sp & 31);
+      w[u] = sp < n ? (sp < 32 ? a : b) : 0.f;
+      const float4* src = reinterpret_cast<const float4*>(part_o + (sp * rows_total + row) * DDT_D_LATENT);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[u][k] = w[u] != 0.f ? src[lane + 32 * k] : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        acc[4 * k] += w[u] * v[u][k].x;
+        acc[4 * k + 1] += w[u] * v[u][k].y;
+        acc[4 * k + 2] += w[u] * v[u][k].z;
+        acc[4 * k + 3] += w[u] * v[u][k].w;
+      }
+    }
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  uint2* dst = reinterpret_cast<uint2*>(out + row * DDT_D_LATENT);
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    dst[lane + 32 * k] = make_uint2(pack_bf16x2(acc[4 * k] * inv, acc[4 * k + 1] * inv),
+                                    pack_bf16x2(acc[4 * k + 2] * inv, acc[4 * k + 3] * inv));
+  if (lse && lane == 0) lse[row] = sum == 0.f ? -INFINITY : top + __logf(sum);
+}
+
+// Most chunks of a request that a call may use: one where the items fill the CTA pairs
+// anyhow or the caches are short (partials and their merge cost about as much as three
+// tiles), else enough to fill them a few times over, within the tiles.
+int q8_max_splits(const ddt_attn_q8_args& a, int sm_count) {
+  if (a.B > vq::kMaxSortedB) return 1;
+  if (a.num_splits > 0) return a.num_splits;
+  const int64_t slots = sm_count / 2 > 0 ? sm_count / 2 : 1;
+  const int64_t items = static_cast<int64_t>(a.B) * ((a.q_len + 1) / 2);
+  const int64_t tiles = (static_cast<int64_t>(a.max_prefix) + a.q_len + vq::kTK - 1) / vq::kTK;
+  if (items >= slots || a.B > vq::kMaxSplitB || tiles < 8) return 1;
+  const int64_t most = 4 * slots / items + 1 < tiles ? 4 * slots / items + 1 : tiles;
+  return static_cast<int>(most < 32 ? most : 32);
+}
+
+size_t q8_workspace_bytes(const ddt_attn_q8_args& a, int max_splits) {
+  if (max_splits <= 1) return 0;
+  const size_t rows = static_cast<size_t>(a.B) * a.q_len * 64;
+  return 256 + static_cast<size_t>(max_splits) * rows * (DDT_D_LATENT + 1) * sizeof(float);
+}
+
+ddt_status launch_verify_attn_q8(const ddt_attn_q8_args& a, int max_splits, void* workspace,
+                                 cudaStream_t stream) {
   using namespace vq;
   const ddt_q8_cache& c = a.cache;
   const uint64_t pages = static_cast<uint64_t>(c.num_pages);
-  const bool partials = num_splits > 1;
-  const int64_t items = static_cast<int64_t>(a.B) * ((a.q_len + 1) / 2) * num_splits;
-  if (items > 0x3fffffffll) return DDT_ERR_UNSUPPORTED;
+  const int64_t rows = static_cast<int64_t>(a.B) * a.q_len * 64;
+  const int64_t items = static_cast<int64_t>(a.B) * ((a.q_len + 1) / 2) * max_splits;
+  if (items > 0x3fffffffll || (rows + 7) / 8 > INT_MAX) return DDT_ERR_UNSUPPORTED;
   // With one page its stride is never taken, but the map wants one.
   const uint64_t lat_page = c.num_pages > 1 ? c.ckv_page_stride : kPage * c.ckv_row_stride;
   const uint64_t rope_page = c.num_pages > 1 ? c.kr_page_stride : kPage * c.kr_row_stride;
   CUtensorMap m_lat, m_rope;
   const bool ok = make_map(&m_lat, c.c_kv, DDT_D_LATENT, kPage, pages, c.ckv_row_stride, lat_page, kPage,
-                     CU_TENSOR_MAP_DATA_TYPE_UINT8, 128) &&
-            make_map(&m_rope, c.k_rope, DDT_D_ROPE, kPage, pages, c.kr_row_stride, rope_page, kPage,
-                     CU_TENSOR_MAP_DATA_TYPE_UINT8, 64, CU_TENSOR_MAP_SWIZZLE_64B);
+                           CU_TENSOR_MAP_DATA_TYPE_UINT8, 128) &&
+                  make_map(&m_rope, c.k_rope, DDT_D_ROPE, kPage, pages, c.kr_row_stride, rope_page, kPage,
+                           CU_TENSOR_MAP_DATA_TYPE_UINT8, 64, CU_TENSOR_MAP_SWIZZLE_64B);
   if (!ok) return DDT_ERR_INVALID_ARG;
   if (ensure_smem_limit(reinterpret_cast<const void*>(verify_attn_q8_kernel), kSmemBytes, 6) !=
       cudaSuccess)
@@ -926,32 +1139,26 @@ ddt_status launch_verify_attn_q8(const ddt_attn_q8_args& a, int num_splits, floa
   p.mask = a.mask;
   p.out = static_cast<uint16_t*>(a.out);
   p.lse = a.lse;
-  p.part_o = part_o;
-  p.part_lse = part_lse;
+  p.chunk = static_cast<int32_t*>(workspace);
+  p.part_o = max_splits > 1 ? reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + 256) : nullptr;
+  p.part_lse = max_splits > 1 ? p.part_o + max_splits * rows * DDT_D_LATENT : nullptr;
   p.status = a.status;
   p.B = a.B;
   p.Q = a.q_len;
   p.num_pages = c.num_pages;
   p.max_blocks = c.max_blocks;
-  p.num_splits = num_splits;
   p.n_pairs = (a.q_len + 1) / 2;
-  p.write_partials = partials;
+  p.max_splits = max_splits;
+  p.forced = a.num_splits > 0;
   p.scale_log2 = a.softmax_scale * kLog2e;
   const int64_t slots = device_sm_count() / 2 > 0 ? device_sm_count() / 2 : 1;
   const int64_t grid = 2 * (items < slots ? items : slots);
-  verify_attn_q8_kernel<<<static_cast<unsigned>(grid), kThreads, kSmemBytes, stream>>>(m_lat, m_rope,
-                                                                                      p);
+  verify_attn_q8_kernel<<<static_cast<unsigned>(grid), kThreads, kSmemBytes, stream>>>(m_lat, m_rope, p);
   if (cudaGetLastError() != cudaSuccess) return DDT_ERR_CUDA;
-  if (!partials) return DDT_OK;
-  ddt_attn_args merge = {};
-  merge.B = a.B;
-  merge.q_len = a.q_len;
-  merge.capacity = c.max_blocks * kPage;
-  merge.prefix_lens = a.prefix_lens;
-  merge.out = a.out;
-  merge.out_dtype = DDT_BF16;
-  merge.lse = a.lse;
-  return launch_verify_merge(merge, num_splits, 0, part_o, part_lse, stream);
+  if (max_splits <= 1) return DDT_OK;
+  verify_merge_q8_kernel<<<static_cast<unsigned>((rows + 7) / 8), 256, 0, stream>>>(
+      p.part_o, p.part_lse, p.chunk, a.prefix_lens, p.out, a.lse, a.B, a.q_len, c.max_blocks);
+  return cudaGetLastError() == cudaSuccess ? DDT_OK : DDT_ERR_CUDA;
 }
 
 cudaError_t q8_fault_flags(uint32_t* flags, bool reset) {

@@ -1,6 +1,6 @@
 // verify_shared.cuh — what the two verify kernels (bf16 and paged 8-bit cache) have in
-// common: the split of a cache into tile ranges, the static schedule of work items over
-// CTA pairs, and the encoding of tensor maps.
+// common: the static schedule of work items over CTA pairs and the encoding of tensor
+// maps.
 #pragma once
 
 #include <cuda.h>
@@ -9,17 +9,7 @@
 #include <cstdint>
 #include <mutex>
 
-#include "ddt_internal.h"
-
 namespace ddt {
-
-// KV tile range [t0, t1) of split `split` for a cache of T rows.
-__host__ __device__ inline void split_range(int T, int num_splits, int split, int& t0, int& t1) {
-  const int n_tiles = (T + kVerifyTileKeys - 1) / kVerifyTileKeys;
-  const int per = (n_tiles + num_splits - 1) / num_splits;
-  t0 = split * per;
-  t1 = t0 + per < n_tiles ? t0 + per : n_tiles;
-}
 
 // The k-th work index of a cluster: rounds of n_clusters indices, alternating
 // direction ("snake"), so that with items sorted by decreasing cost each pair

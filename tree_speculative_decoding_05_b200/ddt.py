@@ -590,7 +590,7 @@ def _attn_q8_args(q_lat, q_rope, c_kv, k_rope, scales, block_table, prefix_lens,
 def verify_attn_q8_workspace_size(q_lat, q_rope, c_kv, k_rope, scales, block_table, prefix_lens,
                                   mask, softmax_scale, max_prefix: int,
                                   num_splits: int = 0) -> tuple[int, int]:
-    """(workspace bytes, number of KV splits) the call will use."""
+    """(workspace bytes, most KV splits) of the call."""
     a = _attn_q8_args(q_lat, q_rope, c_kv, k_rope, scales, block_table, prefix_lens, mask,
                       softmax_scale, max_prefix, num_splits)
     lib = load()
