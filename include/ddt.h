@@ -568,7 +568,10 @@ DDT_API ddt_status ddt_kv_pages(const int32_t* prefix_lens, const int32_t* row_s
  * NULL).  status int32 [B] or NULL: DDT_REQ_NOT_FINITE, or DDT_REQ_BAD_LENGTH
  * (n_b < 0, n_b > max_rows or rows outside [0, n_rows)), DDT_REQ_BAD_PREFIX,
  * DDT_REQ_BAD_INDEX (a page index of its rows), which write nothing for that
- * request.  B = 0 or max_rows = 0 is a no-op (a given status is set). */
+ * request.  B = 0 or max_rows = 0 is a no-op (a given status is set).
+ * Errors: negative sizes, a bad cache, NULL or misaligned pointers ->
+ * DDT_ERR_INVALID_ARG; B * (max_rows / 64 + 2) past 2^31 - 1 ->
+ * DDT_ERR_UNSUPPORTED. */
 DDT_API ddt_status ddt_kv_write_q8(const ddt_q8_cache* cache, const int32_t* prefix_lens,
                           const int32_t* row_start, int32_t B, int32_t q_len, int32_t max_rows,
                           int64_t n_rows, const void* rows_ckv, const void* rows_krope,

@@ -711,6 +711,105 @@ def test_decode_loop_captured_and_on_another_stream():
     follow(loop, d, results)
 
 
+def test_attention_long_ragged_whole_output():
+    """Long ragged caches, every row of the output, against elementary operations in 64
+    bits on the device."""
+    rng = np.random.RandomState(47)
+    Q, prefix = 33, [6000, 5, 2900, 4100, 640, 63, 1, 3333]
+    B, width = len(prefix), 96
+    pages = sum(-(-(p + Q) // PAGE) for p in prefix)
+    table = np.full((B, width), -1, np.int64)
+    perm, at = rng.permutation(pages), 0
+    for b, P in enumerate(prefix):
+        n = -(-(P + Q) // PAGE)
+        table[b, :n] = perm[at:at + n]
+        at += n
+    g = torch.Generator(device="cuda").manual_seed(5)
+    raw = (torch.randn((pages, PAGE, 576), generator=g, device="cuda") * 90).clamp(-448, 448).to(torch.float8_e4m3fn)
+    scales = 2.0 ** torch.randint(-8, -4, (pages,), generator=g, device="cuda").float()
+    mask, vis = tree_mask(random_parents(rng, B, Q))
+    q, ql, qr = queries(rng, B, Q)
+    status = torch.full((B,), -9, dtype=torch.int32, device="cuda")
+    out, lse = ddt.verify_attn_q8(ql, qr, raw[..., :512], raw[..., 512:], scales, i32(table), i32(prefix), mask, SCALE,
+                                  max_prefix=6100, want_lse=True, status=status)
+    assert status.tolist() == [0] * B and ddt.fault_flags() == 0
+    num = den = 0.0
+    for b, P in enumerate(prefix):
+        n = -(-(P + Q) // PAGE)
+        ids = torch.from_numpy(table[b, :n]).cuda()
+        key = (raw.view(torch.uint8)[ids].view(torch.float8_e4m3fn).double() * scales[ids].double()[:, None, None]).flatten(0, 1)[:P + Q]
+        s = q[b].cuda().double().flatten(0, 1) @ key.T * SCALE
+        seen = torch.ones((Q, P + Q), dtype=torch.bool, device="cuda")
+        seen[:, P:] = torch.from_numpy(vis[b]).cuda()
+        s = s.view(Q, 64, P + Q).masked_fill(~seen[:, None, :], -torch.inf)
+        w = torch.softmax(s, 2).flatten(0, 1)
+        o = (w @ key[:, :512]).view(Q, 64, 512)
+        err = (out[b].double() - o).abs()
+        # the terms of q8_reference.error_bound: scores off by at most 4e-3 (a bound over
+        # these inputs: 2^-17 * 5 * 576 * 10 * SCALE and 640 * 2^-24 * 576 * 5 * 10 * SCALE);
+        # each weight times its page's scale off by at most 2^-14 of the row's largest, so
+        # the sum of weight * value by that times the sum of the values' magnitudes
+        mean = (w @ key[:, :512].abs()).view(Q, 64, 512)
+        step = scales[ids].double().repeat_interleave(PAGE)[:P + Q]
+        quantum = 2.0 ** -14 * (w * step).amax(1).view(Q, 64, 1) * (key[:, :512].abs() / step[:, None]).sum(0)
+        assert bool((err <= (2.0 ** -8 + 8e-3) * mean + 2.0 ** -8 * o.abs() + quantum).all())
+        assert float((lse[b].double() - torch.logsumexp(s, 2)).abs().max()) <= 4e-3
+        num, den = num + float((err ** 2).sum()), den + float((o ** 2).sum())
+    assert (num / den) ** 0.5 <= 5e-3
+
+
+def test_attention_replayed_with_other_lengths():
+    """One captured call, replayed as the lengths on the device change: the cut into chunks
+    follows them."""
+    rng = np.random.RandomState(59)
+    Q, most = 2, [1500, 1500, 1500]
+    paged = Paged(rng, [p + Q for p in most])
+    mask, vis = tree_mask(random_parents(rng, 3, Q))
+    q, ql, qr = queries(rng, 3, Q)
+    prefix = i32(most)
+    args = (ql, qr, *paged.args(), prefix, mask, SCALE)
+    ddt.verify_attn_q8(*args, max_prefix=1500)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse = ddt.verify_attn_q8(*args, max_prefix=1500, want_lse=True)
+    for lens in (most, [3, 1400, 700], [0, 0, 1], [1500, 2, 127]):
+        prefix.copy_(i32(lens))
+        graph.replay()
+        check_attention(paged, lens, q, vis, out, lse)
+
+
+def test_attention_requests_share_pages():
+    """Requests with a common prefix read the same pages."""
+    rng = np.random.RandomState(61)
+    Q, prefix = 4, [200, 200, 200]
+    paged = Paged(rng, [p + Q for p in prefix])
+    paged.table[1:, :3] = paged.table[0, :3]
+    paged.dtable = i32(paged.table)
+    mask, vis = tree_mask(random_parents(rng, 3, Q))
+    q, ql, qr = queries(rng, 3, Q)
+    out, lse = ddt.verify_attn_q8(ql, qr, *paged.args(), i32(prefix), mask, SCALE, max_prefix=200, want_lse=True)
+    check_attention(paged, prefix, q, vis, out, lse)
+
+
+def test_calls_on_a_given_stream_keep_their_buffers():
+    """Outputs and workspace that a call allocates for a given stream, dropped at once."""
+    rng = np.random.RandomState(67)
+    Q, prefix = 1, [3000, 2000]
+    paged = Paged(rng, [p + Q for p in prefix])
+    vis = np.ones((2, 1, 1), bool)
+    q, ql, qr = queries(rng, 2, Q)
+    side, pre, mask = torch.cuda.Stream(), i32(prefix), words(vis)
+    out = torch.empty_like(ql)
+    lse = torch.empty((2, Q, 64), device="cuda")
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(20):
+        ddt.verify_attn_q8(ql, qr, *paged.args(), pre, mask, SCALE, max_prefix=3000, out=out, lse=lse, stream=side)
+        torch.full((8 << 20,), 1e9, device="cuda")     # would land in a workspace given back too soon
+    torch.cuda.current_stream().wait_stream(side)
+    check_attention(paged, prefix, q, vis, out, lse)
+
+
 def test_two_streams_at_once_give_the_same():
     rng = np.random.RandomState(51)
     Q, prefix = 9, [2000, 900, 40]

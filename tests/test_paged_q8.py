@@ -81,7 +81,7 @@ def attn_args(**over):
     ({"num_splits": -1}, ddt.DDT_ERR_INVALID_ARG), ({"q_lat": None}, ddt.DDT_ERR_INVALID_ARG),
     ({"q_rope": None}, ddt.DDT_ERR_INVALID_ARG), ({"mask": None}, ddt.DDT_ERR_INVALID_ARG),
     ({"out": None}, ddt.DDT_ERR_INVALID_ARG), ({"prefix_lens": None}, ddt.DDT_ERR_INVALID_ARG),
-    ({"q_lat": FAKE + 2}, ddt.DDT_ERR_INVALID_ARG), ({"out": FAKE + 8}, ddt.DDT_ERR_INVALID_ARG),
+    ({"q_lat": FAKE + 2}, ddt.DDT_ERR_INVALID_ARG), ({"out": FAKE + 16}, ddt.DDT_ERR_INVALID_ARG),
     ({"softmax_scale": 0.0}, ddt.DDT_ERR_INVALID_ARG), ({"softmax_scale": float("nan")}, ddt.DDT_ERR_INVALID_ARG),
     ({"softmax_scale": float("inf")}, ddt.DDT_ERR_INVALID_ARG),
     ({"cache": good_cache(max_blocks=1), "q_len": 65}, ddt.DDT_ERR_INVALID_ARG),
@@ -101,6 +101,7 @@ def test_other_refusals(lib):
         assert write(**bad) == ddt.DDT_ERR_INVALID_ARG, bad
     assert lib.ddt_kv_write_q8(None, FAKE, None, 2, 5, 0, 10, FAKE, FAKE, None, None) == ddt.DDT_ERR_INVALID_ARG
     assert write(B=0) == ddt.DDT_OK
+    assert write(B=1 << 20, q=1 << 20) == ddt.DDT_ERR_UNSUPPORTED
     compact = lambda B=2, q=5, p=FAKE: lib.ddt_kv_compact_q8(c, p, p, p, B, q, None, None, None)  # noqa: E731
     assert compact(B=-1) == compact(p=None) == ddt.DDT_ERR_INVALID_ARG
     assert compact(q=0) == compact(q=129) == ddt.DDT_ERR_UNSUPPORTED
@@ -113,11 +114,11 @@ def test_split_bound_and_workspace(lib):
         return lib.ddt_verify_attn_q8_num_splits(a), lib.ddt_verify_attn_q8_workspace_size(a)
 
     assert of(B=64, q_len=33, max_prefix=4096) == (1, 0)         # enough items without cutting
-    for kw in (dict(B=1, q_len=33, max_prefix=32768), dict(B=64, q_len=1, max_prefix=4096), dict(B=1, q_len=9, max_prefix=256)):
+    for kw in (dict(B=1, q_len=33, max_prefix=32768), dict(B=64, q_len=1, max_prefix=4096), dict(B=1, q_len=9, max_prefix=1000)):
         s, ws = of(**kw)
         tiles = -(-(kw["max_prefix"] + kw["q_len"]) // 128)
         assert 1 < s <= min(32, tiles) and ws == 256 + s * kw["B"] * kw["q_len"] * 64 * 513 * 4
-    assert of(B=1, q_len=1, max_prefix=100)[0] == 1              # one tile
+    assert of(B=1, q_len=9, max_prefix=256)[0] == 1              # few tiles
     assert of(B=3, q_len=5, max_prefix=10, num_splits=7) == (7, 256 + 7 * 3 * 5 * 64 * 513 * 4)
     assert of(B=513, q_len=1, max_prefix=4096, num_splits=4) == (1, 0)
     assert of(B=0) == (1, 0) and of(q_len=0) == (1, 0)

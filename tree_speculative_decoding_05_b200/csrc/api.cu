@@ -416,6 +416,9 @@ ddt_status ddt_kv_write_q8(const ddt_q8_cache* cache, const int32_t* prefix_lens
   if (!q8_cache_ok(*cache) || !prefix_lens) return DDT_ERR_INVALID_ARG;
   if (max_rows > 0 && n_rows > 0 && (!rows_ckv || !rows_krope)) return DDT_ERR_INVALID_ARG;
   if (!aligned16(rows_ckv) || !aligned16(rows_krope)) return DDT_ERR_INVALID_ARG;
+  // one CTA per page that a request's rows may reach
+  if ((static_cast<int64_t>(max_rows) / DDT_PAGE_ROWS + 2) * B > INT32_MAX)
+    return DDT_ERR_UNSUPPORTED;
   if (launch_kv_write_q8(*cache, prefix_lens, row_start, B, q_len, max_rows, n_rows,
                          static_cast<const uint16_t*>(rows_ckv),
                          static_cast<const uint16_t*>(rows_krope), status,

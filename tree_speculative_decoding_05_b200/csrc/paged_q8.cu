@@ -674,7 +674,6 @@ cudaError_t launch_kv_write_q8(const ddt_q8_cache& c, const int32_t* prefix_lens
   // status of an empty request is written).
   const int64_t pages = (static_cast<int64_t>(max_rows) + 2 * kPage - 2) / kPage;
   const int64_t per = pages > 0 ? pages : 1;
-  if (per * B > INT_MAX) return cudaErrorInvalidValue;
   const unsigned ctas = static_cast<unsigned>(per * B);
   if (per > 1 && per <= kMaxWriteCluster)
     return launch_cluster(kv_write_q8_kernel<true>, ctas, static_cast<int>(per), kWriteThreads,
