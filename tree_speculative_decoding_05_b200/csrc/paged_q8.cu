@@ -70,9 +70,10 @@ __device__ __forceinline__ int cluster_rank() {
 // Page plan.  The state (tables, counts, the stack) is small and every request's
 // place on the stack depends on all requests before it, so each CTA scans the
 // requests for itself, 1024 at a time, and the CTAs of one cluster share the page
-// numbers to be moved and the slots; nothing depends on the order in which threads
-// run.  Latency-bound: a handful of dependent loads, two block scans and the page
-// numbers themselves.
+// numbers to be moved; nothing depends on the order in which threads run.
+// Latency-bound: a handful of dependent loads, two block scans and the page numbers
+// themselves (64 requests x 33 rows: 5 us; 1000 prompts of 1 to 2048 rows, 16000 pages
+// and a million slots: 12.5 us a call, 24 us with one CTA).
 // ---------------------------------------------------------------------------
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanCtas = 8;  // of a large plan
@@ -334,8 +335,11 @@ __device__ __forceinline__ int row_step(const ddt_q8_cache& c, int v) {
 // page's new rows (at most 64 x 1152 bytes of bf16) into registers, all loads in
 // flight together, takes their largest magnitude, and stores them at the scale
 // that follows: one pass over the data, bound by memory for prompts and by the
-// latency of load, reduction and store for a step's rows.  Pages that only get
-// rows of their own request need no other CTA's result.
+// latency of load, reduction and store for a step's rows.  No page needs another's
+// result.  Measured: 24 prompts of 1 to 4001 rows (83 MB) 18.5 us, 4.5 TB/s = 0.68 of
+// the measured HBM rate, the two pages that fit an SM's registers taking turns at
+// loading, the maximum and storing (three staged in shared memory: 20.5 us); 64
+// requests x 33 rows 3.9 us.
 // ---------------------------------------------------------------------------
 // The CTAs of a request that reaches few pages (kCluster, at most kMaxWriteCluster) are
 // one cluster: the first one sets the status before the cluster's barrier, the others
@@ -507,7 +511,10 @@ __global__ void __launch_bounds__(kWriteThreads, 1024 / kWriteThreads) kv_write_
 // all read into shared memory before any byte is written, so the gather is race-free
 // for any path.  The scales of the at most three pages that rows move into are known
 // from the pages' present scales alone, without a look at the values: a scale only ever
-// rises, to the largest among the rows that come in.
+// rises, to the largest among the rows that come in.  Measured: 1024 requests, 62 rows
+// moving in each (72 MB), 15.9 us, 4.5 TB/s = 0.69 of the measured HBM rate; 64 requests
+// x 8 rows 3 us (launch, then four dependent loads).  Three column slices of a request,
+// clustered so that one may store the scales: 20 us, for the barriers' sake.
 // ---------------------------------------------------------------------------
 constexpr int kMoveThreads = 256;
 constexpr int kMoveRows = kMoveThreads / kRowVec8;  // 7 rows at a time

@@ -10,12 +10,13 @@
 // key is ever converted; the other operand of each product is split instead:
 //   * q = 2^e (hi + lo) with e4m3 hi and lo, e from the row's largest magnitude.  bf16
 //     has 8 significant bits, hi takes 4 of them and lo the rest, so the split is exact
-//     down to 2^-19 of the row's maximum (e4m3's smallest step against 448).
+//     down to half a step of e4m3's subnormals, 2^-17 of the row's maximum.
 //   * the weights w_j = S_j exp(s_j - m) likewise, hi + lo: relative error 2^-8 as a bf16
 //     weight has.  S_j rides in the exponent (log2 S_j is added to the score), so a page's
 //     scale costs nothing per key; the row sum takes sum(w_j of a page) / S_page.
-//     Weights are held at 2^6 .. 2^8.75 for the largest one so far: steps of e4m3 below
-//     its normal range are 2^-9, so the smallest weights keep 2^-16 of the largest.
+//     Weights are held at 2^4 .. 2^8.75 for the largest one so far: steps of e4m3 below
+//     its normal range are 2^-9, so the smallest weights are off by at most 2^-14 of the
+//     largest.  Scores, sums, the output and the log-sum-exp stay in fp32.
 // Two e4m3 passes cost what one bf16 pass does (twice the rate, half the bytes).  One
 // pass would halve the tensor work and be 2.6 % off per weight, where a bf16 result
 // allows 0.4 %.
@@ -34,17 +35,30 @@
 //     rows before the page's first with zeros and never reads those behind the sequence,
 //     which may hold anything.
 //   * TMEM per CTA: four S buffers (4 x 64 columns) + O (256 columns).
-//   * warps 0-7 softmax, two threads for each half row (32 keys each); 8 and 12 fill the
-//     K rings of even and odd tiles, 10 the V ring; 9, 14 issue S of even and odd tiles
-//     and 11 issues P V (on three sub-partitions); 13 checks a request's page numbers for
-//     its status; 15-18 split the next item's queries while this one's last tiles are at
-//     work, and then write this item's output while the softmax warps go on to the next.
-//   * S runs up to three tiles ahead of the softmax; O is rescaled only when the running
-//     maximum outgrows its reference by 2^2.75.
+//   * warps 0-7 softmax, two threads for each half row (32 keys each): with one, its 64
+//     exponentials and splits outlast a tile's MMAs (64 requests x 33 nodes x 4096 rows:
+//     1225 us back to back, 1098 us with two).  8 and 12 fill the K rings of even and odd
+//     tiles, 10 the V ring; 9 and 14 issue S of even and odd tiles and 11 issues P V, each
+//     as a whole warp with one lane elected: descriptors then stay in uniform registers
+//     and an MMA goes out every 32 cycles, its own time, where a lone lane's loop manages
+//     one in 68 (985 -> 912 us burst).  13 checks a request's page numbers for its status;
+//     15-18 split the next item's queries while this one's last tiles are at work, and
+//     then write this item's output while the softmax warps go on to the next.
+//   * S runs up to four tiles ahead of the softmax; O is rescaled only when the running
+//     maximum outgrows its reference by 2^4.75 (by 2^2.75: 918 us burst, so: 864).
 //   * work items are chunks of a request's tiles for a pair of nodes.  The host knows only
 //     a bound on the lengths, so the chunk is chosen on the device, by every CTA alike,
-//     from the lengths themselves (see make_plan); a request of one chunk is written
-//     directly, the others as normalised partials that a second kernel merges.
+//     from the lengths themselves (plan_cost); a request of one chunk is written directly,
+//     the others as normalised partials that a second kernel merges (64 single tokens over
+//     caches of 1 to 4096 rows: 58 us uncut, 49 us).
+//
+// What bounds it.  64 x 33 x 4096: 876-900 us in a burst, 1.32-1.38 PFLOP/s = 0.80-0.84 of
+// the measured bf16 GEMM burst; 980-1040 us back to back under the 1 kW power cap, 0.84-0.89
+// of the sustained GEMM.  A tile takes 2300-2400 cycles against 2176 of its MMAs (36 x 32 +
+// 16 x 64): the softmax of the slower CTA of the pair sets the pace, and an item costs
+// 5000-6000 cycles more (its queries are split only once S no longer reads the last ones).
+// Short caches and few requests are bound by latency: 15 us for one request x 9 x 256,
+// of which launch and plan 3, queries 5, a tile's chain of S, softmax and P V 3, output 2.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
