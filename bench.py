@@ -110,10 +110,11 @@ TRAFFIC_RECORD = os.path.join(ROOT, "profiles", "verify_attn_config2.json")
 
 
 def kernel_source_hash() -> str:
-    """sha256 of the verify kernel's sources (the kernel file and its PTX header)."""
+    """sha256 of the verify kernel's sources (the kernel file and its headers)."""
     import hashlib
     csrc = os.path.join(ROOT, "tree_speculative_decoding_05_b200", "csrc")
-    src = b"".join(open(os.path.join(csrc, f), "rb").read() for f in ("verify_attn.cu", "sm100_ptx.cuh"))
+    files = ("verify_attn.cu", "sm100_ptx.cuh", "verify_shared.cuh")
+    src = b"".join(open(os.path.join(csrc, f), "rb").read() for f in files)
     return hashlib.sha256(src).hexdigest()
 
 
