@@ -792,6 +792,36 @@ def test_attention_requests_share_pages():
     check_attention(paged, prefix, q, vis, out, lse)
 
 
+@pytest.mark.parametrize("splits", [0, 3])
+def test_attention_prefix_past_the_stated_bound(splits):
+    """max_prefix only plans the cut: longer requests are answered all the same."""
+    rng = np.random.RandomState(71 + splits)
+    Q, prefix = 3, [2500, 700, 5]
+    paged = Paged(rng, [p + Q for p in prefix])
+    mask, vis = tree_mask(random_parents(rng, 3, Q))
+    q, ql, qr = queries(rng, 3, Q)
+    for bound in (0, 1100):
+        out, lse = ddt.verify_attn_q8(ql, qr, *paged.args(), i32(prefix), mask, SCALE, max_prefix=bound,
+                                      want_lse=True, num_splits=splits)
+        check_attention(paged, prefix, q, vis, out, lse)
+
+
+def test_no_requests():
+    none = lambda *shape, dtype=torch.int32: torch.empty(shape, dtype=dtype, device="cuda")  # noqa: E731
+    bf16 = torch.bfloat16
+    cache = (none(4, 64, 512, dtype=torch.float8_e4m3fn), none(4, 64, 64, dtype=torch.float8_e4m3fn),
+             torch.ones(4, device="cuda"), none(0, 3))
+    free, count = i32([0, 1, 2, 3]), i32([4])
+    slots, status = ddt.kv_pages(none(0), none(0, 3), none(0), free, count, q_len=5)
+    assert slots.numel() == status.numel() == 0 and count.tolist() == [4]
+    assert ddt.kv_write_q8(*cache, none(0), none(0, 5, 512, dtype=bf16), none(0, 5, 64, dtype=bf16)).numel() == 0
+    out, lse = ddt.verify_attn_q8(none(0, 5, 64, 512, dtype=bf16), none(0, 5, 64, 64, dtype=bf16), *cache, none(0),
+                                  none(0, 5, 1, dtype=torch.int64), SCALE, max_prefix=9, want_lse=True)
+    assert out.shape == (0, 5, 64, 512) and lse.shape == (0, 5, 64)
+    new, status = ddt.kv_compact_q8(*cache, none(0), none(0, 5), none(0))
+    assert new.numel() == status.numel() == 0
+
+
 def test_calls_on_a_given_stream_keep_their_buffers():
     """Outputs and workspace that a call allocates for a given stream, dropped at once."""
     rng = np.random.RandomState(67)
@@ -854,6 +884,9 @@ def test_binding_refusals_on_the_device():
             ddt.kv_write_q8(c, k, s, t, p, *bad)
     with pytest.raises(ddt.DdtError):
         ddt.kv_write_q8(c, k, s, t, p, rows[0][0], rows[1][0], row_start=i32([0, 1, 3]))
+    for most in (-1, 1 << 31, (1 << 32) + 3):
+        with pytest.raises(ddt.DdtError):
+            ddt.kv_write_q8(c, k, s, t, p, rows[0][0], rows[1][0], row_start=i32([0, 1, 3]), max_rows=most)
     path = i32([[0, 1, 2], [0, 1, 2]])
     for bad in ((path[:, :2], p), (path.long(), p), (path, p[:1])):
         with pytest.raises(ddt.DdtError):

@@ -567,6 +567,8 @@ def kv_write_q8(c_kv: torch.Tensor, k_rope: torch.Tensor, scales: torch.Tensor,
     else:
         if max_rows is None:
             raise DdtError("row_start needs max_rows")
+        if not 0 <= max_rows < 1 << 31:
+            raise DdtError(f"max_rows must be a row count, got {max_rows}")
         n, q = _dims(rows_ckv, 2, "rows_ckv")[0], 0
         lat, rope = (n, D_LATENT), (n, D_ROPE)
     if status is None:
