@@ -336,9 +336,9 @@ __device__ __forceinline__ int row_step(const ddt_q8_cache& c, int v) {
 // flight together, takes their largest magnitude, and stores them at the scale
 // that follows: one pass over the data, bound by memory for prompts and by the
 // latency of load, reduction and store for a step's rows.  No page needs another's
-// result.  Measured: 24 prompts of 1 to 4001 rows (83 MB) 18.5 us, 4.5 TB/s = 0.68 of
+// result.  Measured: 24 prompts of 1 to 4001 rows (83 MB) 17.1 us, 4.9 TB/s = 0.74 of
 // the measured HBM rate, the two pages that fit an SM's registers taking turns at
-// loading, the maximum and storing (three staged in shared memory: 20.5 us); 64
+// loading, the maximum and storing (three staged in shared memory: 2 us slower); 64
 // requests x 33 rows 3.9 us.
 // ---------------------------------------------------------------------------
 // The CTAs of a request that reaches few pages (kCluster, at most kMaxWriteCluster) are
@@ -453,6 +453,17 @@ __device__ __forceinline__ int write_page(const ddt_q8_cache& c, PageRows& rows,
   return any_odd;
 }
 
+// The write starts while this runs and waits for its end before it touches a status, so
+// the statuses are cleared behind the pages' loads (24 prompts: 20.4 us after a memset,
+// 17.1 so; the plan's slots and the attention's merge gained nothing from it).
+__global__ void kv_clear_status_kernel(int32_t* status, int B) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int64_t b = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  if (b < B) status[b] = DDT_REQ_OK;
+}
+
+__device__ __forceinline__ void await_clear() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 template <bool kCluster>
 __global__ void __launch_bounds__(kWriteThreads, 1024 / kWriteThreads) kv_write_q8_kernel(
     const ddt_q8_cache c, const int32_t* __restrict__ prefix_lens,
@@ -489,11 +500,13 @@ __global__ void __launch_bounds__(kWriteThreads, 1024 / kWriteThreads) kv_write_
   }
   if (__syncthreads_or(bad)) s.status = DDT_REQ_BAD_INDEX;
   if (s.status != DDT_REQ_OK) {
+    if (!kCluster) await_clear();
     if (k == 0 && t == 0 && status) status[b] = s.status;
     return;
   }
   int any_odd = 0;
   if (n > 0) any_odd = write_page(c, rows, table[blk0 + k], static_cast<int>(lo - page0), n, s_max);
+  if (!kCluster) await_clear();
   if (!status) return;
   if (t == 0 && k == 0 && (kCluster || pages_per_request == 1))
     status[b] = any_odd ? DDT_REQ_NOT_FINITE : DDT_REQ_OK;
@@ -625,21 +638,29 @@ __global__ void __launch_bounds__(kMoveThreads) kv_compact_q8_kernel(
 // Launchers
 // ---------------------------------------------------------------------------
 namespace {
-// A launch of `ctas` CTAs in clusters of `cluster`.
+// A launch in clusters of `cluster` CTAs, or (early) one that may start before the kernel
+// ahead of it has ended, once that one's CTAs have said so.
 template <typename... Params, typename... Args>
-cudaError_t launch_cluster(void (*kernel)(Params...), unsigned ctas, int cluster, int threads,
-                           cudaStream_t stream, Args... args) {
+cudaError_t launch_with(void (*kernel)(Params...), unsigned ctas, int cluster, bool early,
+                        int threads, cudaStream_t stream, Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(threads);
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = cluster;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  if (cluster > 1) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    attr[cfg.numAttrs].val.clusterDim.x = cluster;
+    attr[cfg.numAttrs].val.clusterDim.y = 1;
+    attr[cfg.numAttrs].val.clusterDim.z = 1;
+    ++cfg.numAttrs;
+  }
+  if (early) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+    ++cfg.numAttrs;
+  }
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -660,9 +681,9 @@ cudaError_t launch_kv_pages(const int32_t* prefix_lens, const int32_t* row_start
         free_pages, n_free, slots, status);
     e = cudaGetLastError();
   } else {
-    e = launch_cluster(kv_pages_kernel<kPlanCtas>, kPlanCtas, kPlanCtas, kPlanThreads, stream,
-                       prefix_lens, row_start, B, q_len, slot_rows, num_pages, max_blocks,
-                       block_table, n_blocks, free_pages, n_free, slots, status);
+    e = launch_with(kv_pages_kernel<kPlanCtas>, kPlanCtas, kPlanCtas, false, kPlanThreads, stream,
+                    prefix_lens, row_start, B, q_len, slot_rows, num_pages, max_blocks, block_table,
+                    n_blocks, free_pages, n_free, slots, status);
   }
   if (e != cudaSuccess || !slots || fused) return e;
   const int64_t ctas = (n_rows + kSlotRows - 1) / kSlotRows;
@@ -683,18 +704,19 @@ cudaError_t launch_kv_write_q8(const ddt_q8_cache& c, const int32_t* prefix_lens
   const int64_t per = pages > 0 ? pages : 1;
   const unsigned ctas = static_cast<unsigned>(per * B);
   if (per > 1 && per <= kMaxWriteCluster)
-    return launch_cluster(kv_write_q8_kernel<true>, ctas, static_cast<int>(per), kWriteThreads,
-                          stream, c, prefix_lens, row_start, q_len, max_rows, n_rows, rows_ckv,
-                          rows_krope, status, static_cast<int>(per));
+    return launch_with(kv_write_q8_kernel<true>, ctas, static_cast<int>(per), false, kWriteThreads,
+                       stream, c, prefix_lens, row_start, q_len, max_rows, n_rows, rows_ckv,
+                       rows_krope, status, static_cast<int>(per));
   // The statuses of long prompts start at OK; a page's CTA can only raise its request's.
-  if (status && per > 1) {
-    const cudaError_t e = cudaMemsetAsync(status, 0, static_cast<size_t>(B) * sizeof(int32_t), stream);
+  const bool cleared = status && per > 1;
+  if (cleared) {
+    kv_clear_status_kernel<<<static_cast<unsigned>((B + 255) / 256), 256, 0, stream>>>(status, B);
+    const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  kv_write_q8_kernel<false><<<ctas, kWriteThreads, 0, stream>>>(
-      c, prefix_lens, row_start, q_len, max_rows, n_rows, rows_ckv, rows_krope, status,
-      static_cast<int>(per));
-  return cudaGetLastError();
+  return launch_with(kv_write_q8_kernel<false>, ctas, 1, cleared, kWriteThreads, stream, c,
+                     prefix_lens, row_start, q_len, max_rows, n_rows, rows_ckv, rows_krope, status,
+                     static_cast<int>(per));
 }
 
 cudaError_t launch_kv_compact_q8(const ddt_q8_cache& c, const int32_t* prefix_lens,
