@@ -52,14 +52,6 @@ __device__ __forceinline__ Span load_span(const int32_t* prefix_lens, const int3
   return s;
 }
 
-// Cluster barrier in two halves: what a CTA wrote (or read) before its arrival lies
-// before what any CTA does after its wait.
-__device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 __device__ __forceinline__ int cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));

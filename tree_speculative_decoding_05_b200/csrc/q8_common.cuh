@@ -1,5 +1,6 @@
-// q8_common.cuh — how bf16 values find their power-of-two e4m3 scale, shared by the
-// quantising write and the split of the attention's queries.
+// q8_common.cuh — shared by the kernels of the paged 8-bit cache: how bf16 values find
+// their power-of-two e4m3 scale (the quantising write, the split of the attention's
+// queries), and the cluster barrier in two halves.
 #pragma once
 
 #include <cstdint>
@@ -24,6 +25,15 @@ __device__ __forceinline__ int e4m3_exponent(uint32_t amax_bits) {
 
 __device__ __forceinline__ float pow2f(int e) {  // -126 <= e <= 127
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+}
+
+// Cluster barrier in two halves: what a CTA wrote (or read) before its arrival lies
+// before what any CTA does after its wait.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 }  // namespace ddt
