@@ -159,7 +159,7 @@ struct Params {
   const uint64_t* mask;
   uint16_t* out;
   float* lse;
-  float* part_o;    // [num_splits][B * Q * 64][512]
+  float* part_o;    // [num_splits][B * Q * 64][512], see part_offset
   float* part_lse;  // [num_splits][B * Q * 64]
   int32_t* status;
   int32_t* chunk;   // the chunk chosen, for the merge
