@@ -300,6 +300,38 @@ def test_write_not_finite():
             assert not np.isnan(ref.DECODE[paged.cache[paged.table[b, pos // PAGE], pos % PAGE]]).any()
 
 
+def test_write_statuses_of_long_prompts():
+    """More pages a request than a cluster takes: statuses raised by any page, over whatever
+    stood there, eagerly and in a replayed graph."""
+    rng = np.random.RandomState(73)
+    lens, prefix = [300, 5, 0, 700, 260, 66, 520], np.array([10, 63, 5, 0, 64, 200, 1])
+    paged = Paged(rng, [int(p) + max(n, 1) for p, n in zip(prefix, lens)], exps=(-9,))
+    paged.table[4, 3] = -1                       # a page that is none
+    paged.to_device()
+    rows = rows_of(rng, lens)
+    rows[0][0, 5], rows[3][699, 575], rows[3][640, 0], rows[5][30, 3] = np.nan, np.inf, -np.inf, np.nan
+    flat = torch.from_numpy(np.concatenate(rows)).to(torch.bfloat16).cuda()
+    lat, rope = flat[:, :512].contiguous(), flat[:, 512:].contiguous()
+    start, pre = i32(np.concatenate([[0], np.cumsum(lens)])), i32(prefix)
+    status = i32([99, -7, 8, 3, 0, 1, 55])
+    call = lambda: ddt.kv_write_q8(*paged.args(), pre, lat, rope, row_start=start, max_rows=700, status=status)  # noqa: E731
+    call()
+    want = ref.write(paged.cache, paged.scales, paged.table, [int(p) for p in prefix], rows)
+    assert want == [ref.NOT_FINITE, 0, 0, ref.NOT_FINITE, ref.BAD_INDEX, ref.NOT_FINITE, 0]
+    assert status.tolist() == want
+    paged.check()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for _ in range(3):
+        status.fill_(77)
+        graph.replay()
+        assert status.tolist() == want
+    # the same rows again, at scales that no longer change but for pages written from their start
+    ref.write(paged.cache, paged.scales, paged.table, [int(p) for p in prefix], rows)
+    paged.check()
+
+
 def test_write_refused_requests_change_nothing():
     rng = np.random.RandomState(5)
     rows = rows_of(rng, [70, 70, 70, 70])
