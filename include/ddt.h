@@ -489,9 +489,9 @@ DDT_API ddt_status ddt_decode_step(const ddt_decode_args* args, ddt_stream_t str
  * that only read may share them); a page index outside [0, num_pages) is never
  * followed, and gives DDT_REQ_BAD_INDEX where a call needs that page.
  *
- * Strides are in elements (= bytes), multiples of 16, of rows below 2^31 and of pages
- * below 2^40; bases are 16-byte aligned; a row is 512 / 64 contiguous values.  One allocation of 576-byte rows serves
- * both arrays (k_rope = c_kv + 512). */
+ * Strides are in elements (= bytes), multiples of 16, of rows below 2^31 and of
+ * pages below 2^40; bases are 16-byte aligned; a row is 512 / 64 contiguous values.
+ * One allocation of 576-byte rows serves both arrays (k_rope = c_kv + 512). */
 #define DDT_PAGE_ROWS 64
 
 typedef struct ddt_q8_cache {

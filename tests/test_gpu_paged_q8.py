@@ -824,6 +824,22 @@ def test_attention_requests_share_pages():
     check_attention(paged, prefix, q, vis, out, lse)
 
 
+@pytest.mark.parametrize("last", [8191, 9000])
+def test_attention_many_chunks(last):
+    """As many chunks as may be forced (64 of one tile, or 36 of two), merged, and a request
+    of a few of them beside."""
+    rng = np.random.RandomState(last)
+    prefix = [last, 1300, 100]
+    paged = Paged(rng, [p + 1 for p in prefix], exps=(-8, -7))
+    q, ql, qr = queries(rng, 3, 1)
+    vis = np.ones((3, 1, 1), bool)
+    out, lse = ddt.verify_attn_q8(ql, qr, *paged.args(), i32(prefix), words(vis), SCALE, max_prefix=last,
+                                  want_lse=True, num_splits=64)
+    check_attention(paged, prefix, q, vis, out, lse)
+    plain, _ = ddt.verify_attn_q8(ql, qr, *paged.args(), i32(prefix), words(vis), SCALE, max_prefix=last, num_splits=64)
+    assert torch.equal(plain, out)
+
+
 @pytest.mark.parametrize("splits", [0, 3])
 def test_attention_prefix_past_the_stated_bound(splits):
     """max_prefix only plans the cut: longer requests are answered all the same."""
