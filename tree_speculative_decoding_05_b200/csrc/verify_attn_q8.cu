@@ -11,12 +11,16 @@
 //   * q = 2^e (hi + lo) with e4m3 hi and lo, e from the row's largest magnitude.  bf16
 //     has 8 significant bits, hi takes 4 of them and lo the rest, so the split is exact
 //     down to half a step of e4m3's subnormals, 2^-17 of the row's maximum.
-//   * the weights w_j = S_j exp(s_j - m) likewise, hi + lo: relative error 2^-8 as a bf16
-//     weight has.  S_j rides in the exponent (log2 S_j is added to the score), so a page's
-//     scale costs nothing per key; the row sum takes sum(w_j of a page) / S_page.
-//     Weights are held at 2^4 .. 2^8.75 for the largest one so far: steps of e4m3 below
-//     its normal range are 2^-9, so the smallest weights are off by at most 2^-14 of the
-//     largest.  Scores, sums, the output and the log-sum-exp stay in fp32.
+//   * the weights w_j = S_j exp(s_j - m) as hi (e4m3) + lo (e5m2, whose range is wider):
+//     relative error 2^-8 as a bf16 weight has, and where hi runs out of range, below 2^-6,
+//     at most 2^-14 absolute.  m follows the tiles' largest weights, up and down, so that
+//     each tile's lies between 2^-4 and 2^8.75 (see kBase): small weights are kept however
+//     many there are and whatever outweighs them.  S_j rides in the exponent (log2 S_j is
+//     added to the score), so a page's scale costs nothing per key; the row sum takes
+//     sum(w_j of a page) / S_page.  It adds the weights before they are rounded (adding
+//     the rounded ones would take two more conversions a pair): a row whose weights are
+//     all off in one direction is off by as much, 2^-8 at most.  Scores, sums, the output
+//     and the log-sum-exp stay in fp32.
 // Two e4m3 passes cost what one bf16 pass does (twice the rate, half the bytes).  One
 // pass would halve the tensor work and be 2.6 % off per weight, where a bf16 result
 // allows 0.4 %.
@@ -44,8 +48,9 @@
 //     one in 68 (985 -> 912 us burst).  13 checks a request's page numbers for its status;
 //     15-18 split the next item's queries while this one's last tiles are at work, and
 //     then write this item's output while the softmax warps go on to the next.
-//   * S runs up to four tiles ahead of the softmax; O is rescaled only when the running
-//     maximum outgrows its reference by 2^4.75 (by 2^2.75: 918 us burst, so: 864).
+//   * S runs up to four tiles ahead of the softmax; O is rescaled only when a tile's
+//     maximum outgrows its reference by 2^4.75 (by 2^2.75: 918 us burst, so: 864) or falls
+//     2^8 short of it.
 //   * work items are chunks of a request's tiles for a pair of nodes.  The host knows only
 //     a bound on the lengths, so the chunk is chosen on the device, by every CTA alike,
 //     from the lengths themselves (plan_cost); a request of one chunk is written directly,
@@ -140,14 +145,30 @@ static_assert((2 * kMaxSortedB + 64 + kThreads / 32 * (kMaxSplitB / 2 * 3)) * 4 
 
 constexpr int kTmemCols = 512, kTmemS = 0, kTmemO = 256;
 constexpr uint32_t kIdescQK = idesc_e4m3_f32(128, kTK, false);
-constexpr uint32_t kIdescPV = idesc_e4m3_f32(128, 256, true);
+constexpr uint32_t kIdescPVHi = idesc_e4m3_f32(128, 256, true);
+constexpr uint32_t kIdescPVLo = kIdescPVHi | 1u << 7;  // A in e5m2 (format 1)
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-// The reference weight 2^kBase and the growth kSlack allowed before O is rescaled:
-// 2^(4 + 4.75) = 431 <= 448.  Rescaling costs a wait for P V and a pass over O, and any
-// row of a warp's 32 causes it: for normally distributed scores (deviation 1.7) two rows
-// in five outgrow 2^2.75 between the first tile and the 33rd, one in thirty 2^4.75.  The
-// steps at the bottom are then 2^-13 of the largest weight.
-constexpr float kBase = 4.0f, kSlack = 4.75f;
+// A weight is held as a multiple of a unit of its row, 2^(m_ref - kBase), and is precise to
+// 2^-8 from 2^-6 units on; below, steps are coarser and end at 2^-16.  The unit therefore
+// follows the scores, both ways:
+//   * up, when a tile's largest weight would pass 2^(kBase + kSlack) = 431 (of 448);
+//   * down, when it would lie below 2^(kBase - kDrop) = 2^-4, as behind an attention sink,
+//     whose weight may be 2^20 times one of the thousands that follow it and carry the
+//     result.  O and the row sum then grow by that power, in fp32, which has room: the unit
+//     stays within 2^-kDeep of the largest it was (|O| < 2^30 rows x 2^(kDeep + 9) x 448).
+//     A tile of tree rows alone does not lower it: a node sees few of them, at 2^-14 each,
+//     and would pay a pass over O at every item's end (1 x 9 x 256: 16.0 against 15.4 us,
+//     64 x 33 x 4096 1 % slower);
+//   * a tile whose largest weight is 2^kPeak times that of some other 32 of its keys puts it
+//     at 2^8.5 units rather than 2^4, for the sake of the keys beside it.
+// A change of unit costs a wait for P V and a pass over O, and any row of a warp's 32 causes
+// it: for normally distributed scores (deviation 1.7) two rows in five outgrow 2^2.75 between
+// the first tile and the 33rd, one in thirty 2^4.75, and falls by 2^8 are as rare.  Next to a
+// unit that only rises and a lo in e4m3, which lost whole tails (a sink of 0.8 over 4096
+// alike rows: the result 97 % off): 64 x 33 x 4096 881 -> 891 us, 64 x 65 over <= 8192 rows of
+// uneven magnitude 1829 -> 1928, 1 x 9 x 256 15.2 -> 15.4.
+constexpr float kBase = 4.0f, kSlack = 4.75f, kDrop = 8.0f, kDeep = 48.0f;
+constexpr float kPeak = 8.0f, kPeakBase = 4.5f;
 constexpr float kMinScale = 9.094947017729282e-13f;  // 2^-40
 
 struct Params {
@@ -285,18 +306,21 @@ __device__ __forceinline__ void block_coords(const Params& p, const Block& k, in
   page = ok ? k.page : 0;
 }
 
-// Two floats (lo in the low half) as the sum of two e4m3 pairs.  fp16 keeps 11 bits and
-// the residual of the first rounding exactly; the values lie within 448.
-__device__ __forceinline__ void split_e4m3x2(float lo, float hi, uint16_t& first,
-                                             uint16_t& second) {
-  asm("{\n\t.reg .b32 x, y, z;\n\t"
+// Two floats (lo in the low half) as the sum of two pairs, the first e4m3, the second e4m3
+// or e5m2.  fp16 keeps 11 bits and the residual of the first rounding exactly; the values
+// lie within 448.
+template <bool kWideSecond>
+__device__ __forceinline__ void split_f8x2(float lo, float hi, uint16_t& first, uint16_t& second) {
+  uint32_t z;
+  asm("{\n\t.reg .b32 x, y;\n\t"
       "cvt.rn.f16x2.f32 x, %3, %2;\n\t"
       "cvt.rn.satfinite.e4m3x2.f16x2 %0, x;\n\t"
       "cvt.rn.f16x2.e4m3x2 y, %0;\n\t"
-      "sub.rn.f16x2 z, x, y;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f16x2 %1, z;\n\t}"
-      : "=h"(first), "=h"(second)
+      "sub.rn.f16x2 %1, x, y;\n\t}"
+      : "=h"(first), "=r"(z)
       : "f"(lo), "f"(hi));
+  if constexpr (kWideSecond) asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(second) : "r"(z));
+  else asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(second) : "r"(z));
 }
 
 __device__ __forceinline__ uint32_t pack16(uint16_t lo, uint16_t hi) {
@@ -328,7 +352,7 @@ __device__ __forceinline__ void split_row(const uint32_t (&x)[9], uint8_t* q, in
 #pragma unroll
     for (int v = 0; v < (j < 4 ? 2 : 1); ++v) {
       const uint32_t h = mul_bf16x2(x[2 * j + v], inv);
-      split_e4m3x2(__uint_as_float(h << 16), __uint_as_float(h & 0xffff0000u), f[v], f[2 + v]);
+      split_f8x2<false>(__uint_as_float(h << 16), __uint_as_float(h & 0xffff0000u), f[v], f[2 + v]);
     }
     hi[j] = pack16(f[0], f[1]);
     lo[j] = pack16(f[2], f[3]);
@@ -715,8 +739,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(vq::kThreads, 1)
             for (int ks = 0; ks < 2; ++ks) {
               const uint64_t pd = p_desc + ((kPage * (i >> 1) + 32 * ks) >> 4);
               const uint64_t vd = v_desc + ((4096 * ks) >> 4);
-              if (one) mma_f8_ss<2>(d, pd, vd, kIdescPV, jj > 0 || i >= 2 || ks > 0);
-              if (one) mma_f8_ss<2>(d, pd + (kBox >> 4), vd, kIdescPV, 1);
+              if (one) mma_f8_ss<2>(d, pd, vd, kIdescPVHi, jj > 0 || i >= 2 || ks > 0);
+              if (one) mma_f8_ss<2>(d, pd + (kBox >> 4), vd, kIdescPVLo, 1);
             }
             if (one) mma_commit<2>(bar(kBarVEmpty + r.stage), 0x3);
             r.advance(kVSlots);
@@ -921,8 +945,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(vq::kThreads, 1)
           __uint_as_float(static_cast<uint32_t>(q_scale[slot * 64 + m]) << 16) * p.scale_log2;
       ++iter;
       float m_ref = -INFINITY;  // log2 units, page scale included
+      float m_low = -INFINITY;  // the reference falls no further
       float l_sum = 0.f;
-      float m_use = 0.f;
       for (int jj = 0; jj < it.ntile; ++jj, ++G) {
         const int sb = static_cast<int>(G & 1);
         const int pbuf = static_cast<int>(G % kPBufs);
@@ -981,16 +1005,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(vq::kThreads, 1)
         mx = fmaxf(fmaxf(red[m], red[64 + m]), fmaxf(red[128 + m], red[192 + m]));
         float factor = 1.f;
         bool rescale = false;
-        if (m_ref == -INFINITY) {
-          m_ref = mx;
-        } else if (mx > m_ref + kSlack) {
-          factor = fast_exp2(m_ref - mx);
-          m_ref = mx;
-          l_sum *= factor;
-          rescale = true;
+        // mx - m_ref outside [-kDrop, kSlack] (false where both are -inf)
+        if (fabsf(mx - m_ref + 0.5f * (kDrop - kSlack)) > 0.5f * (kDrop + kSlack)) {
+          const float least = fminf(fminf(red[m], red[64 + m]), fminf(red[128 + m], red[192 + m]));
+          float next = mx - least > kPeak ? mx - kPeakBase : mx;
+          if (mx < m_ref)  // not for a tile of tree rows alone, nor one that shows no key
+            next = kPage * (blk - hf) >= P || mx == -INFINITY ? m_ref : fmaxf(next, m_low);
+          if (m_ref != -INFINITY && next != m_ref) {
+            factor = fast_exp2(m_ref - next);
+            l_sum *= factor;
+            rescale = true;
+          }
+          m_ref = next;
+          m_low = fmaxf(m_low, m_ref - kDeep);
         }
-        m_use = m_ref == -INFINITY ? 0.f : m_ref;
-        const float shift = lk - m_use + kBase;
+        const float shift = lk - (m_ref == -INFINITY ? 0.f : m_ref) + kBase;
         uint32_t hi[8], lo[8];
         float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -1002,7 +1031,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(vq::kThreads, 1)
             const float e1 = fast_exp2(fmaf(x[4 * c + 2 * v + 1], sc, shift));
             part[2 * v] += e0;
             part[2 * v + 1] += e1;
-            split_e4m3x2(e0, e1, f[v], f[2 + v]);
+            split_f8x2<true>(e0, e1, f[v], f[2 + v]);
           }
           hi[c] = pack16(f[0], f[1]);
           lo[c] = pack16(f[2], f[3]);
@@ -1044,7 +1073,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(vq::kThreads, 1)
       // The row sums and their reference go to the output warps.
       float* red = red_l + (iter - 1) % kLSlots * kRedL;
       red[part_of] = l_sum;
-      if (t < 64) red[256 + m] = m_use;
+      if (t < 64) red[256 + m] = m_ref == -INFINITY ? 0.f : m_ref;
       mbar_arrive_local(bar(kBarL + (iter - 1) % kLSlots));
     }
   }
