@@ -455,11 +455,19 @@ def _launch(fn, what: str, dev: int, stream, *args) -> None:
         _check(rc, what)
 
 
-def _kept(t: torch.Tensor, stream) -> torch.Tensor:
-    """A tensor allocated here that a call on `stream` uses: its memory is not given out
-    again before that call is done, even if the caller drops it at once."""
-    if stream is not None:
-        t.record_stream(stream)
+def _new(stream, returned: bool, make, *args, **kwargs) -> torch.Tensor:
+    """make(*args, **kwargs), a buffer for a call on `stream` (None: the current one).  It
+    comes from the memory of that stream, where whoever had it last is done before the call
+    begins, and where whoever has it next begins after the call; memory of the current
+    stream may still be in use there by work that the given stream does not wait for.  A
+    returned one is also kept from being given out before the current stream, on which the
+    caller may read it, is done with it."""
+    if stream is None:
+        return make(*args, **kwargs)
+    with torch.cuda.stream(stream):
+        t = make(*args, **kwargs)
+    if returned:
+        t.record_stream(torch.cuda.current_stream(t.device))
     return t
 
 
@@ -531,9 +539,9 @@ def kv_pages(prefix_lens: torch.Tensor, block_table: torch.Tensor, n_blocks: tor
     i32 = torch.int32
     width, pages = _dims(block_table, 2, "block_table")[1], _dims(free_pages, 1, "free_pages")[0]
     if slots is None:
-        slots = _kept(torch.empty(n_rows, dtype=torch.int64, device=prefix_lens.device), stream)
+        slots = _new(stream, True, torch.empty, n_rows, dtype=torch.int64, device=prefix_lens.device)
     if status is None:
-        status = _kept(torch.empty_like(prefix_lens), stream)
+        status = _new(stream, True, torch.empty_like, prefix_lens)
     _launch(load().ddt_kv_pages, "ddt_kv_pages", dev, stream,
             _arg(prefix_lens, "prefix_lens", i32, (B,), dev),
             _arg(row_start, "row_start", i32, (B + 1,), dev), B, q_len or 0, n_rows, pages, width,
@@ -572,7 +580,7 @@ def kv_write_q8(c_kv: torch.Tensor, k_rope: torch.Tensor, scales: torch.Tensor,
         n, q = _dims(rows_ckv, 2, "rows_ckv")[0], 0
         lat, rope = (n, D_LATENT), (n, D_ROPE)
     if status is None:
-        status = _kept(torch.empty_like(prefix_lens), stream)
+        status = _new(stream, True, torch.empty_like, prefix_lens)
     _launch(load().ddt_kv_write_q8, "ddt_kv_write_q8", dev, stream,
             _q8_cache(c_kv, k_rope, scales, block_table, B, dev),
             _arg(prefix_lens, "prefix_lens", i32, (B,), dev),
@@ -624,9 +632,9 @@ def verify_attn_q8(q_lat: torch.Tensor, q_rope: torch.Tensor, c_kv: torch.Tensor
                       softmax_scale, max_prefix, num_splits)
     dev, (B, Q, H, _) = c_kv.get_device(), q_lat.shape
     if out is None:  # of q_lat's shape and type
-        out = _kept(torch.empty_like(q_lat), stream)
+        out = _new(stream, True, torch.empty_like, q_lat)
     if lse is None and want_lse:
-        lse = _kept(torch.empty((B, Q, H), dtype=torch.float32, device=c_kv.device), stream)
+        lse = _new(stream, True, torch.empty, (B, Q, H), dtype=torch.float32, device=c_kv.device)
     a.out = _arg(out, "out", torch.bfloat16, (B, Q, H, D_LATENT), dev)
     a.lse = _arg(lse, "lse", torch.float32, (B, Q, H), dev)
     a.status = _arg(status, "status", torch.int32, (B,), dev)
@@ -634,7 +642,7 @@ def verify_attn_q8(q_lat: torch.Tensor, q_rope: torch.Tensor, c_kv: torch.Tensor
     if workspace is None:
         need = lib.ddt_verify_attn_q8_workspace_size(a)
         if need:
-            workspace = _kept(torch.empty(need, dtype=torch.uint8, device=c_kv.device), stream)
+            workspace = _new(stream, False, torch.empty, need, dtype=torch.uint8, device=c_kv.device)
     if workspace is not None:
         if workspace.get_device() != dev:
             raise DdtError(f"workspace must be on cuda:{dev}")
@@ -653,9 +661,9 @@ def kv_compact_q8(c_kv: torch.Tensor, k_rope: torch.Tensor, scales: torch.Tensor
     (new_prefix_lens, status)."""
     dev, (B, Q), i32 = _device_of(c_kv, "c_kv"), _dims(path, 2, "path"), torch.int32
     if new_prefix_lens is None:
-        new_prefix_lens = _kept(torch.empty_like(prefix_lens), stream)
+        new_prefix_lens = _new(stream, True, torch.empty_like, prefix_lens)
     if status is None:
-        status = _kept(torch.empty_like(prefix_lens), stream)
+        status = _new(stream, True, torch.empty_like, prefix_lens)
     _launch(load().ddt_kv_compact_q8, "ddt_kv_compact_q8", dev, stream,
             _q8_cache(c_kv, k_rope, scales, block_table, B, dev),
             _arg(prefix_lens, "prefix_lens", i32, (B,), dev),
