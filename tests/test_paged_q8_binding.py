@@ -1,12 +1,18 @@
 """What the binding of the paged calls does around a launch, on the CPU with the launch
 itself taken out: where the buffers that a call makes for itself come from."""
 import contextlib
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
 
 from tree_speculative_decoding_05_b200 import build as ddt_build
 from tree_speculative_decoding_05_b200 import ddt
+
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def i32(*shape):
@@ -69,3 +75,22 @@ def test_buffers_come_from_the_given_stream(monkeypatch, name, given):
     # what is handed out lives until the stream that the caller is on is done with it too
     kept = [t.data_ptr() for t, s in recorded if s == "current"]
     assert sorted(kept) == (sorted(t.data_ptr() for t in got) if given else [])
+
+
+def test_binding_loads_without_the_raw_stream_lookup():
+    """A torch that lacks the short way to the current stream still imports the binding, and
+    takes the public way."""
+    code = """
+import torch
+if hasattr(torch._C, "_cuda_getCurrentRawStream"):
+    del torch._C._cuda_getCurrentRawStream
+from tree_speculative_decoding_05_b200 import ddt
+class Stream:
+    cuda_stream = 42
+torch.cuda.current_stream = lambda dev=None: Stream if dev == 3 else None
+torch.cuda.current_device = lambda: 3
+seen = []
+ddt._launch(lambda *a: seen.append(a) or ddt.DDT_OK, "what", 3, None, 7, 8)
+assert seen == [(7, 8, 42)], seen
+"""
+    subprocess.run([sys.executable, "-c", code], cwd=ROOT, check=True)

@@ -439,7 +439,9 @@ def decode_step(args: DecodeArgs, stream=None) -> None:
 # The paged 8-bit latent cache
 # ---------------------------------------------------------------------------
 
-_raw_stream = torch._C._cuda_getCurrentRawStream  # (device index) -> cudaStream_t
+# (device index) -> cudaStream_t; the public way makes a Stream object first
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _launch(fn, what: str, dev: int, stream, *args) -> None:
