@@ -60,6 +60,7 @@ def test_buffers_come_from_the_given_stream(monkeypatch, name, given):
     launched = []
     monkeypatch.setattr(ddt, "_device_of", lambda t, name: -1)          # as the tensors say here
     monkeypatch.setattr(ddt, "_launch", lambda *a: launched.append((a, tuple(entered))))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)
     monkeypatch.setattr(torch.cuda, "stream", stream_context)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: "current")
     monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: recorded.append((t, s)), raising=False)
@@ -94,3 +95,36 @@ ddt._launch(lambda *a: seen.append(a) or ddt.DDT_OK, "what", 3, None, 7, 8)
 assert seen == [(7, 8, 42)], seen
 """
     subprocess.run([sys.executable, "-c", code], cwd=ROOT, check=True)
+
+
+def test_workspace_is_sized_on_the_tensors_device(monkeypatch):
+    """How far a call may be cut depends on the SMs of the device that it runs on, which need
+    not be the current one: the size is asked there, as the launch asks again."""
+    ddt_build.build()
+    lib, current, asked = ddt.load(), [7], []
+
+    @contextlib.contextmanager
+    def device_context(d):
+        current.append(d.index if isinstance(d, torch.device) else d)
+        yield
+        current.pop()
+
+    class Lib:
+        def __getattr__(self, name):
+            def call(*args):
+                asked.append((name, current[-1]))
+                return 0 if name == "ddt_verify_attn_q8" else getattr(lib, name)(*args)
+            return call
+
+    monkeypatch.setattr(ddt, "_device_of", lambda t, name: -1)      # as the tensors say here
+    monkeypatch.setattr(ddt, "load", Lib)
+    monkeypatch.setattr(ddt, "_raw_stream", lambda dev: 0)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current[-1])
+    monkeypatch.setattr(torch.cuda, "device", device_context)
+    args = (bf16(2, 5, 64, 512), bf16(2, 5, 64, 64), *CACHE, i32(2), torch.ones(2, 5, 1, dtype=torch.int64), 0.07)
+    ddt.verify_attn_q8(*args, max_prefix=1000)
+    size, splits = ddt.verify_attn_q8_workspace_size(*args, max_prefix=1000)
+    assert [n for n, _ in asked] == ["ddt_verify_attn_q8_workspace_size", "ddt_verify_attn_q8",
+                                     "ddt_verify_attn_q8_workspace_size", "ddt_verify_attn_q8_num_splits"]
+    assert all(d == -1 for _, d in asked), asked
+    assert size > 0 and splits > 1 and current == [7]

@@ -444,15 +444,17 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
-def _launch(fn, what: str, dev: int, stream, *args) -> None:
-    """fn(*args, stream) on device `dev`, whatever device is current (and stays so), on
-    its current stream or the given one."""
-    s = _raw_stream(dev) if stream is None else stream.cuda_stream
+def _on(dev: int, fn, *args):
+    """fn(*args) on device `dev`, whatever device is current (and stays so)."""
     if dev == torch.cuda.current_device():
-        rc = fn(*args, s)
-    else:
-        with torch.cuda.device(dev):
-            rc = fn(*args, s)
+        return fn(*args)
+    with torch.cuda.device(dev):
+        return fn(*args)
+
+
+def _launch(fn, what: str, dev: int, stream, *args) -> None:
+    """fn(*args, stream) on device `dev`, on its current stream or the given one."""
+    rc = _on(dev, fn, *args, _raw_stream(dev) if stream is None else stream.cuda_stream)
     if rc != DDT_OK:
         _check(rc, what)
 
@@ -613,10 +615,9 @@ def verify_attn_q8_workspace_size(q_lat, q_rope, c_kv, k_rope, scales, block_tab
     """(workspace bytes, most KV splits) of the call."""
     a = _attn_q8_args(q_lat, q_rope, c_kv, k_rope, scales, block_table, prefix_lens, mask,
                       softmax_scale, max_prefix, num_splits)
-    lib = load()
-    with torch.cuda.device(c_kv.device):
-        return (int(lib.ddt_verify_attn_q8_workspace_size(a)),
-                int(lib.ddt_verify_attn_q8_num_splits(a)))
+    lib, dev = load(), c_kv.get_device()
+    return (int(_on(dev, lib.ddt_verify_attn_q8_workspace_size, a)),
+            int(_on(dev, lib.ddt_verify_attn_q8_num_splits, a)))
 
 
 def verify_attn_q8(q_lat: torch.Tensor, q_rope: torch.Tensor, c_kv: torch.Tensor,
@@ -642,7 +643,7 @@ def verify_attn_q8(q_lat: torch.Tensor, q_rope: torch.Tensor, c_kv: torch.Tensor
     a.status = _arg(status, "status", torch.int32, (B,), dev)
     lib = load()
     if workspace is None:
-        need = lib.ddt_verify_attn_q8_workspace_size(a)
+        need = _on(dev, lib.ddt_verify_attn_q8_workspace_size, a)
         if need:
             workspace = _new(stream, False, torch.empty, need, dtype=torch.uint8, device=c_kv.device)
     if workspace is not None:
