@@ -141,7 +141,7 @@ constexpr int kOffAbort = kOffTmemPtr + 4;
 constexpr int kSmemUsed = kOffAbort + 4;
 constexpr int kSmemBytes = kSmemUsed + 1024;  // slack for 1024-byte alignment
 static_assert(kSmemBytes <= 232448, "shared memory budget");
-static_assert((2 * kMaxSortedB + 64 + kThreads / 32 * (kMaxSplitB / 2 * 3)) * 4 <= kPBufs * kPBufBytes, "plan");
+static_assert((2 * kMaxSortedB + 64 + kThreads / 32 * 2 * kMaxSplitB) * 4 <= kPBufs * kPBufBytes, "plan");
 
 constexpr int kTmemCols = 512, kTmemS = 0, kTmemO = 256;
 constexpr uint32_t kIdescQK = idesc_e4m3_f32(128, kTK, false);
@@ -247,13 +247,14 @@ __device__ __forceinline__ Item decode_item(const Params& p, int w, const Plan& 
 // What a choice of chunk costs, in tiles: the longest of the pairs' shares under the
 // schedule that work_index gives, each item counting kItemTiles on top of its tiles
 // (queries, filling and draining the pipeline), and the merge.  By one warp, for requests
-// of tiles[0 .. B); `sorted` has room for 3/2 kMaxSplitB numbers.
+// of tiles[0 .. B); `sorted` has room for 2 kMaxSplitB numbers.  A request has at most 2^23
+// tiles, so a remainder and an index fit into one.
 constexpr float kItemTiles = 4.5f, kMergeTiles = 3.f;
 __device__ float plan_cost(const int* tiles, int B, int n_pairs, int n_clusters, int chunk,
                            int* sorted) {
   const int lane = threadIdx.x & 31;
   int whole = 0, rests = 0;
-  int* key = sorted + kMaxSplitB / 2;  // rest and index in one, so that all differ
+  int* key = sorted + kMaxSplitB;  // rest and index in one, so that all differ
   for (int b = lane; b < B; b += 32) {
     const int n = tiles[b] / chunk, rest = tiles[b] - n * chunk;
     whole += n;
@@ -261,13 +262,12 @@ __device__ float plan_cost(const int* tiles, int B, int n_pairs, int n_clusters,
     key[b] = rest * kMaxSplitB + b;
   }
   __syncwarp();
-  uint16_t* order = reinterpret_cast<uint16_t*>(sorted);
   for (int b = lane; b < B; b += 32) {
     const int mine = key[b];
     int rank = 0;
 #pragma unroll 8
     for (int i = 0; i < B; ++i) rank += key[i] > mine;
-    order[rank] = static_cast<uint16_t>(mine / kMaxSplitB);
+    sorted[rank] = mine / kMaxSplitB;
   }
   whole = __reduce_add_sync(0xffffffffu, whole) * n_pairs;
   const int n = whole + __reduce_add_sync(0xffffffffu, rests) * n_pairs;
@@ -277,7 +277,7 @@ __device__ float plan_cost(const int* tiles, int B, int n_pairs, int n_clusters,
     float share = 0.f;
     for (int k = 0; k * n_clusters < n; ++k) {
       const int w = work_index(k, j, n_clusters, n);
-      if (w >= 0) share += kItemTiles + (w < whole ? chunk : order[n_pairs == 1 ? w - whole : (w - whole) / n_pairs]);
+      if (w >= 0) share += kItemTiles + (w < whole ? chunk : sorted[n_pairs == 1 ? w - whole : (w - whole) / n_pairs]);
     }
     most = fmaxf(most, share);
   }
@@ -489,7 +489,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(vq::kThreads, 1)
       const int most = p.max_splits < longest ? p.max_splits : longest;
       for (int c = warp + 1; c <= most; c += kThreads / 32) {
         const float cost = plan_cost(tiles, p.B, p.n_pairs, n_clusters, (longest + c - 1) / c,
-                                     sorted + warp * (kMaxSplitB / 2 * 3));
+                                     sorted + warp * (2 * kMaxSplitB));
         if (lane == 0) costs[c - 1] = c > 1 ? cost + kMergeTiles : cost;
       }
       __syncthreads();
