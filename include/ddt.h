@@ -599,7 +599,10 @@ DDT_API ddt_status ddt_kv_write_q8(const ddt_q8_cache* cache, const int32_t* pre
  * Splits: a request's cache may be cut into chunks whose partial results are merged.
  * How many is decided on the device from the lengths themselves, at most
  * ddt_verify_attn_q8_num_splits(args); num_splits > 0 forces that many for the longest
- * request (and chunks of that size for the others).  It takes a workspace of
+ * request (and chunks of that size for the others).  No request is cut where there are
+ * more than 512 (num_splits then changes nothing and the requests run as they come), nor,
+ * with num_splits 0, where B * ceil(q_len / 2) reaches half the device's SMs or B passes
+ * 128.  It takes a workspace of
  * ddt_verify_attn_q8_workspace_size(args) bytes, 256-byte aligned; with NULL or less no
  * request is cut.  Calls that may overlap need workspaces of their own.
  * status int32 [B] or NULL: DDT_REQ_BAD_PREFIX (P < 0 or P + q_len > max_blocks *
@@ -624,7 +627,7 @@ typedef struct ddt_attn_q8_args {
   size_t workspace_bytes;
   int32_t* status;    /* int32 [B] or NULL                                      */
   float softmax_scale; /* > 0 and finite                                        */
-  int32_t num_splits; /* 0 = choose on the device; otherwise 1..64              */
+  int32_t num_splits; /* 0 = choose on the device; otherwise 1..64 (B <= 512)   */
 } ddt_attn_q8_args;
 
 /* Bytes of workspace, and the most KV splits the call may use (sizes only; invalid

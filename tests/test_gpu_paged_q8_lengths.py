@@ -6,6 +6,7 @@ import numpy as np
 import pytest
 import torch
 
+from test_gpu_paged_q8 import Paged, check_attention, i32, queries, words
 from tree_speculative_decoding_05_b200 import ddt
 
 pytestmark = pytest.mark.gpu
@@ -42,3 +43,21 @@ def test_cut_of_requests_longer_than_65535_tiles():
     assert float((lse[:, 0].double() - want).abs().max()) <= 65600 * 2.0 ** -24 + 1e-3
     bound = (8 * 65600 * 2.0 ** -23 + 65600 * 2.0 ** -24 + 2.0 ** -7) * (p @ key[:, :512].abs())
     assert bool(((out[:, 0].double() - p @ key[:, :512]).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("B", [512, 513])
+@pytest.mark.parametrize("splits", [0, 3])
+def test_forced_splits_around_512_requests(B, splits):
+    """Past 512 requests none is cut, whatever was asked for, and none is put in order; the
+    results are the same."""
+    rng = np.random.RandomState(B + splits)
+    prefix = [int(x) for x in rng.randint(0, 70, B)]
+    prefix[B // 2], prefix[B - 1] = 900, 640
+    paged = Paged(rng, [p + 1 for p in prefix])
+    q, ql, qr = queries(rng, B, 1)
+    args = (ql, qr, *paged.args(), i32(prefix), words(np.ones((B, 1, 1), bool)), SCALE)
+    status = torch.full((B,), -9, dtype=torch.int32, device="cuda")
+    out, lse = ddt.verify_attn_q8(*args, max_prefix=900, want_lse=True, num_splits=splits, status=status)
+    check_attention(paged, prefix, q, np.ones((B, 1, 1), bool), out, lse)
+    assert status.tolist() == [0] * B
+    assert ddt.verify_attn_q8_workspace_size(*args, max_prefix=900, num_splits=splits)[1] == (3 if splits and B == 512 else 1)

@@ -1171,9 +1171,14 @@ __global__ void __launch_bounds__(256, 3) verify_merge_q8_kernel(
   }
 }
 
-// Most chunks of a request that a call may use: one where the items fill the CTA pairs
-// anyhow or the caches are short (partials and their merge cost about as much as three
-// tiles), else enough to fill them a few times over, within the tiles.
+// Most chunks of a request that a call may use: one past kMaxSortedB requests (the work list
+// is then none), where the items fill the CTA pairs anyhow or the caches are short (partials
+// and their merge cost about as much as three tiles), else enough to fill them a few times
+// over, within the tiles.  Items that fill the pairs are balanced by their order alone where
+// lengths are alike; one request much longer than its batch is not cut there and runs on by
+// itself (128 single tokens, one over 32768 rows and the others over 1024: 261 tiles on one
+// pair against 27 on the average, by plan_cost), since partials are laid out for all rows
+// times all chunks.
 int q8_max_splits(const ddt_attn_q8_args& a, int sm_count) {
   if (a.B > vq::kMaxSortedB) return 1;
   if (a.num_splits > 0) return a.num_splits;

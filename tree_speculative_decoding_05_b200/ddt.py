@@ -629,8 +629,9 @@ def verify_attn_q8(q_lat: torch.Tensor, q_rope: torch.Tensor, c_kv: torch.Tensor
                    status: Optional[torch.Tensor] = None, stream=None):
     """Tree-verify MLA-absorb attention over the paged 8-bit cache (arguments of the cache
     as for kv_write_q8, the others as for verify_attn).  q_len 1 with mask word 1 is a
-    plain decode step.  Returns (out bf16 [B, Q, 64, 512], lse float32 [B, Q, 64] or
-    None)."""
+    plain decode step.  num_splits 0 lets the call choose how far to cut long caches, > 0
+    forces it (up to 512 requests; more are never cut).  Returns (out bf16 [B, Q, 64, 512],
+    lse float32 [B, Q, 64] or None)."""
     a = _attn_q8_args(q_lat, q_rope, c_kv, k_rope, scales, block_table, prefix_lens, mask,
                       softmax_scale, max_prefix, num_splits)
     dev, (B, Q, H, _) = c_kv.get_device(), q_lat.shape
