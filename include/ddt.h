@@ -584,11 +584,12 @@ DDT_API ddt_status ddt_kv_write_q8(const ddt_q8_cache* cache, const int32_t* pre
  * the cache stands for, with the tree block at cache rows P .. P+q_len-1 (q_len 1
  * with mask word 1 is a plain decode step).  Queries are bf16 and enter as the sum
  * of two e4m3 terms under a power-of-two scale per row (exact to 2^-17 of the
- * row's largest value).  Softmax weights enter as an e4m3 and an e5m2 term: off by at
- * most 2^-8 of themselves, as bf16 weights are, or by 2^-10 of the largest among the
- * 128 cache rows around them (rows 128 k .. 128 k + 127; 2^-18 of the largest of all,
- * for rows all of the tree block) where that is more.  Each weight counts in the sum
- * as it was before.  Scores, sums and the output accumulate in fp32.
+ * row's largest value).  Softmax weights, times their pages' scales, enter as an e4m3
+ * and an e5m2 term: off by at most 2^-8 of themselves, as bf16 weights are, or by 2^-10
+ * of the largest such product among the 128 cache rows around them (rows 128 k .. 128 k
+ * + 127; where those are tree rows alone, 2^-18 of the largest of all) where that is
+ * more.  The sum counts each weight as it was before.  Scores, sums and the output
+ * accumulate in fp32.
  *
  * out is bf16 [B, q_len, 64, 512], 32-byte aligned (the weights' 8 bits would not
  * fill an fp32 output), lse fp32 [B, q_len, 64] or NULL, with the meaning of ddt_verify_attn;
