@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_paged_q8 import SCALE, Paged, i32, queries, random_parents, rows_of, tree_mask
+from test_gpu_paged_q8 import SCALE, Paged, check_attention, i32, queries, random_parents, rows_of, tree_mask
 from tree_speculative_decoding_05_b200 import ddt
 
 pytestmark = pytest.mark.gpu
@@ -59,3 +59,34 @@ def test_cache_calls_on_a_side_stream():
     torch.cuda.current_stream().wait_stream(side)
     assert st0.tolist() == st1.tolist() == st2.tolist() == [0, 0, 0]
     assert new.tolist() == [13, 66, 201] and slots.numel() == 27 and int(slots.min()) >= 0
+
+
+def test_captured_calls_on_a_given_stream():
+    """A graph whose capture forks to a side stream that the calls are given, replayed: their
+    buffers belong to the graph."""
+    rng = np.random.RandomState(97)
+    Q, prefix = 3, [4000, 1500]
+    paged = Paged(rng, [p + Q for p in prefix])
+    mask, vis = tree_mask(random_parents(rng, 2, Q))
+    q, ql, qr = queries(rng, 2, Q)
+    pre, side = i32(prefix), torch.cuda.Stream()
+    rows = torch.zeros(2, Q, 512, dtype=torch.bfloat16, device="cuda"), torch.zeros(2, Q, 64, dtype=torch.bfloat16, device="cuda")
+    spare = Paged(rng, [p + Q for p in prefix])
+    call = lambda s: (ddt.verify_attn_q8(ql, qr, *paged.args(), pre, mask, SCALE, max_prefix=4000, want_lse=True, stream=s),  # noqa: E731
+                      ddt.kv_write_q8(*spare.args(), pre, *rows, stream=s))
+    call(None)
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            side.wait_stream(torch.cuda.current_stream())
+            got = call(side)
+            torch.cuda.current_stream().wait_stream(side)
+        graphs.append((g, got))
+    for g, ((out, lse), status) in graphs * 2:
+        out.fill_(3.0), lse.fill_(3.0), status.fill_(3)
+        g.replay()
+        torch.full((32 << 20,), 1e9, device="cuda")
+        check_attention(paged, prefix, q, vis, out, lse)
+        assert status.tolist() == [0, 0]
