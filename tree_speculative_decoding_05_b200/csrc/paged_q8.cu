@@ -328,10 +328,12 @@ __device__ __forceinline__ int row_step(const ddt_q8_cache& c, int v) {
 // flight together, takes their largest magnitude, and stores them at the scale
 // that follows: one pass over the data, bound by memory for prompts and by the
 // latency of load, reduction and store for a step's rows.  No page needs another's
-// result.  Measured: 24 prompts of 1 to 4001 rows (83 MB) 17.1 us, 4.9 TB/s = 0.74 of
-// the measured HBM rate, the two pages that fit an SM's registers taking turns at
-// loading, the maximum and storing (three staged in shared memory: 2 us slower); 64
-// requests x 33 rows 3.9 us.
+// result.  Measured: 24 prompts of 1 to 4001 rows (83 MB) 22.3 us over data outside the
+// L2, 3.7 TB/s = 0.57 of the measured HBM rate, the two pages that fit an SM's registers
+// taking turns at loading, the maximum and storing; 17.3 us repeated on one set of
+// buffers, which the L2 then holds (three pages staged in shared memory: 2 us slower
+// there).  64 requests x 33 rows: 7.7 us with live rows rescaled, 5.1 without, 4.3
+// repeated.
 // ---------------------------------------------------------------------------
 // The CTAs of a request that reaches few pages (kCluster, at most kMaxWriteCluster) are
 // one cluster: the first one sets the status before the cluster's barrier, the others
@@ -446,8 +448,8 @@ __device__ __forceinline__ int write_page(const ddt_q8_cache& c, PageRows& rows,
 }
 
 // The write starts while this runs and waits for its end before it touches a status, so
-// the statuses are cleared behind the pages' loads (24 prompts: 20.4 us after a memset,
-// 17.1 so; the plan's slots and the attention's merge gained nothing from it).
+// the statuses are cleared behind the pages' loads (24 prompts, repeated: 20.4 us after a
+// memset, 17.1 so; the plan's slots and the attention's merge gained nothing from it).
 __global__ void kv_clear_status_kernel(int32_t* status, int B) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int64_t b = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
@@ -517,9 +519,12 @@ __global__ void __launch_bounds__(kWriteThreads, 1024 / kWriteThreads) kv_write_
 // for any path.  The scales of the at most three pages that rows move into are known
 // from the pages' present scales alone, without a look at the values: a scale only ever
 // rises, to the largest among the rows that come in.  Measured: 1024 requests, 62 rows
-// moving in each (72 MB), 15.9 us, 4.5 TB/s = 0.69 of the measured HBM rate; 64 requests
-// x 8 rows 3 us (launch, then four dependent loads).  Three column slices of a request,
-// clustered so that one may store the scales: 20 us, for the barriers' sake.
+// moving in each (74 MB): 29 us over data outside the L2 where scales rise and the rest of
+// those pages is rescaled, 21.6 us (3.4 TB/s = 0.52 of the measured HBM rate) where none
+// does, 16.1 us repeated on one set of buffers, which the L2 then holds.  64 requests x 8
+// rows: 9.7, 4.1 and 3.0 us (launch, then four dependent loads).  Three column slices of a
+// request, clustered so that one may store the scales: 20 against 16 us, for the barriers'
+// sake.
 // ---------------------------------------------------------------------------
 constexpr int kMoveThreads = 256;
 constexpr int kMoveRows = kMoveThreads / kRowVec8;  // 7 rows at a time

@@ -18,7 +18,7 @@
 //     many there are and whatever outweighs them.  S_j rides in the exponent (log2 S_j is
 //     added to the score), so a page's scale costs nothing per key; the row sum takes
 //     sum(w_j of a page) / S_page.  It adds the weights before they are rounded (adding
-//     the rounded ones would take two more conversions a pair): a row whose weights are
+//     the rounded ones takes another conversion and two additions a pair): a row whose weights are
 //     all off in one direction is off by as much, 2^-8 at most.  Scores, sums, the output
 //     and the log-sum-exp stay in fp32.
 // Two e4m3 passes cost what one bf16 pass does (twice the rate, half the bytes).  One
@@ -57,8 +57,8 @@
 //     the others as normalised partials that a second kernel merges (64 single tokens over
 //     caches of 1 to 4096 rows: 58 us uncut, 46 us).
 //
-// What bounds it.  64 x 33 x 4096: 876-900 us in a burst, 1.32-1.38 PFLOP/s = 0.80-0.84 of
-// the measured bf16 GEMM burst; 980-1040 us back to back under the 1 kW power cap, 0.84-0.89
+// What bounds it.  64 x 33 x 4096: 865-895 us in a burst, 1.35-1.40 PFLOP/s = 0.82-0.85 of
+// the measured bf16 GEMM burst; 1000-1035 us back to back under the 1 kW power cap, 0.85-0.88
 // of the sustained GEMM.  A tile takes 2300-2400 cycles against 2176 of its MMAs (36 x 32 +
 // 16 x 64): the softmax of the slower CTA of the pair sets the pace, and an item costs
 // 5000-6000 cycles more (its queries are split only once S no longer reads the last ones).
